@@ -34,6 +34,23 @@ class HCAError(RuntimeError):
         self.code = code
 
 
+class _PagedCache(ctypes.Structure):      # hca_paged_cache_t
+    _fields_ = [(n, ctypes.c_void_p) for n in ("wk", "wv", "ws", "ck", "cv", "page_table")] + [
+        ("table_stride", ctypes.c_longlong), ("max_pages", ctypes.c_int),
+        ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int)]
+
+
+class _PageTable(ctypes.Structure):       # hca_page_table_t
+    _fields_ = [("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_longlong),
+                ("rows", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("n_pages", ctypes.c_void_p), ("ref", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int)]
+
+
+class _PageArray(ctypes.Structure):       # hca_page_array_t
+    _fields_ = [("data", ctypes.c_void_p), ("item_bytes", ctypes.c_longlong)]
+
+
 _LIB = None
 
 
@@ -67,6 +84,19 @@ def lib() -> ctypes.CDLL:
         L.hca_quantize_e4m3.argtypes = [vp, ctypes.c_longlong, vp, vp, vp]
         L.hca_decode_e4m3.argtypes = [vp, vp, vp, vp, vp, i, vp, vp, vp, vp, vp, vp, i, i, f, vp,
                                       sz, vp, vp]
+        pc, pt, pa = (ctypes.POINTER(t) for t in (_PagedCache, _PageTable, _PageArray))
+        L.hca_paged_append.argtypes = [vp, vp, vp, vp, vp, i, i, pc, vp]
+        L.hca_paged_prefill_workspace_size.argtypes = [i, i]
+        L.hca_paged_prefill_workspace_size.restype = sz
+        L.hca_paged_prefill.argtypes = [vp] * 7 + [i, i, i, f, vp, vp, i, pc, vp, vp, sz, vp]
+        L.hca_paged_decode.argtypes = [vp, vp, vp, i, i, f, vp, vp, i, pc, vp, vp, sz, vp]
+        L.hca_paged_decode_step.argtypes = [vp] * 6 + [i, i, f, vp, vp, i, pc, vp, vp, sz, vp]
+        L.hca_pages_workspace_size.argtypes = [i, i, i]
+        L.hca_pages_workspace_size.restype = sz
+        L.hca_pages_resize.argtypes = [pt, vp, vp, sz, vp]
+        L.hca_pages_fork.argtypes = [pt, vp, vp, vp, i, pa, i, pa, i, vp, vp, sz, vp]
+        L.hca_pages_compact.argtypes = [pt, pa, i, vp, vp, sz, vp]
+        L.hca_pages_copy.argtypes = [pa, i, i, vp, vp, i, vp, sz, vp]
         L.hca_get_device_error.argtypes = [vp, ctypes.POINTER(ctypes.c_uint)]
         L.hca_selftest_bounded_wait.argtypes = [i, vp]
         L.hca_status_string.argtypes = [i]
@@ -75,7 +105,10 @@ def lib() -> ctypes.CDLL:
         for name in ("hca_compress", "hca_prefill_fwd", "hca_decode", "hca_get_device_error",
                      "hca_selftest_bounded_wait", "hca_cache_append", "hca_decode_step",
                      "hca_quantize_e4m3", "hca_decode_e4m3", "hca_prefill_fwd_vha",
-                     "hca_decode_vha", "hca_prefill_bwd"):
+                     "hca_decode_vha", "hca_prefill_bwd", "hca_paged_append",
+                     "hca_paged_prefill", "hca_paged_decode", "hca_paged_decode_step",
+                     "hca_pages_resize", "hca_pages_fork", "hca_pages_compact",
+                     "hca_pages_copy"):
             getattr(L, name).restype = i
         _LIB = L
     return _LIB
@@ -398,6 +431,328 @@ def decode_e4m3(q: torch.Tensor, ck: torch.Tensor, ck_scale: torch.Tensor, cv: t
         ctx_len.data_ptr(), g.data_ptr(), S, H, ctypes.c_float(scale), workspace.data_ptr(),
         workspace.numel(), out.data_ptr(), _stream(q.device)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# Paged cache
+# ---------------------------------------------------------------------------
+PAGE_SIZES = (16, 32, 64, 128)
+
+
+def _on(device: torch.device):
+    """The library launches on the current device: make it that of the tensors."""
+    return torch.cuda.device(device)
+
+
+def _check_on(device: torch.device, *tensors):
+    for t, n in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"{n} is on {t.device}, expected {device}")
+
+
+def _check_table(page_table: torch.Tensor, rows: int):
+    """A page table: int32 [rows, max_pages] whose rows may lie apart (a view)."""
+    if not isinstance(page_table, torch.Tensor) or page_table.device.type != "cuda":
+        raise ValueError("page_table must be a tensor on a CUDA device")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != rows:
+        raise ValueError(f"page_table must be int32 [{rows}, max_pages], got "
+                         f"{page_table.dtype} {tuple(page_table.shape)}")
+    cols = page_table.shape[1]
+    if (cols > 1 and page_table.stride(1) != 1) or (rows > 1 and page_table.stride(0) < cols):
+        raise ValueError("page_table's rows must be contiguous and not overlap")
+    return cols, (page_table.stride(0) if rows > 1 else cols)
+
+
+def _paged_cache(S, wk, wv, ws, ck_pages, cv_pages, page_table) -> _PagedCache:
+    _check(wk, "wk", (S, WINDOW, HEAD_DIM))
+    _check(wv, "wv", (S, WINDOW, HEAD_DIM))
+    if ws is not None:
+        _check(ws, "ws", (S, WINDOW))
+    if not isinstance(ck_pages, torch.Tensor) or ck_pages.dim() != 3:
+        raise ValueError("ck_pages must be [num_pages, page_size, 512]")
+    num, size = ck_pages.shape[0], ck_pages.shape[1]
+    if size not in PAGE_SIZES:
+        raise ValueError(f"pages must hold 16, 32, 64 or 128 entries, got {size}")
+    _check(ck_pages, "ck_pages", (num, size, HEAD_DIM))
+    _check(cv_pages, "cv_pages", (num, size, HEAD_DIM))
+    cols, stride = _check_table(page_table, S)
+    _check_on(wk.device, (wv, "wv"), (ws, "ws"), (ck_pages, "ck_pages"), (cv_pages, "cv_pages"),
+              (page_table, "page_table"))
+    return _PagedCache(wk.data_ptr(), wv.data_ptr(), _ptr(ws), ck_pages.data_ptr() if num else None,
+                       cv_pages.data_ptr() if num else None,
+                       page_table.data_ptr() if cols else None, stride, cols, num, size)
+
+
+def _check_chunk(k_new, v_new, s_new, q_start, ctx_len, device):
+    S = ctx_len.shape[0]
+    N = k_new.shape[0]
+    _check(ctx_len, "ctx_len", (S,), dtype=torch.int32)
+    _check(k_new, "k_new", (N, HEAD_DIM))
+    _check(v_new, "v_new", (N, HEAD_DIM))
+    _check(s_new, "s_new", (N,))
+    if q_start is not None:
+        _check(q_start, "q_start", (S + 1,), dtype=torch.int32)
+    elif N != S:
+        raise ValueError(f"{N} new tokens for {S} sequences need q_start")
+    _check_on(device, (ctx_len, "ctx_len"), (k_new, "k_new"), (v_new, "v_new"), (s_new, "s_new"),
+              (q_start, "q_start"))
+    return S, N
+
+
+def _attend_args(q, g, out, vha, rows, scale, device):
+    _check(q, "q", (rows, HEADS, HEAD_DIM))
+    _check(g, "g", (rows, HEADS, HEAD_DIM))
+    if out is None:
+        out = torch.empty_like(q)
+    _check(out, "out", (rows, HEADS, HEAD_DIM))
+    _check_on(device, (q, "q"), (g, "g"), (out, "out"))
+    down, up, r = (None, None, 0) if vha is None else _check_vha(vha, device)
+    return (out, 1.0 / math.sqrt(HEAD_DIM) if scale is None else scale, _ptr(down), _ptr(up), r)
+
+
+def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, s_new: torch.Tensor,
+                 q_start: Optional[torch.Tensor], ctx_len: torch.Tensor, wk: torch.Tensor,
+                 wv: torch.Tensor, ws: torch.Tensor, ck_pages: torch.Tensor,
+                 cv_pages: torch.Tensor, page_table: torch.Tensor) -> None:
+    """Append a chunk of new tokens per sequence to a paged cache, in place.
+
+    k_new, v_new [N, 512]; s_new [N]: the tokens of all sequences, packed;
+    sequence i brings q_start[i] .. q_start[i + 1] - 1 (q_start [S + 1] int32;
+    None: one token each).  ctx_len [S] int32 counts them.  wk, wv
+    [S, 128, 512] and ws [S, 128] rings; ck_pages, cv_pages
+    [num_pages, page_size, 512]; page_table [S, max_pages] int32: entry j of
+    sequence i is row j % page_size of page page_table[i, j // page_size]."""
+    device = wk.device
+    S, N = _check_chunk(k_new, v_new, s_new, q_start, ctx_len, device)
+    cache = _paged_cache(S, wk, wv, ws, ck_pages, cv_pages, page_table)
+    if N == 0:
+        return
+    with _on(device):
+        _ok("hca_paged_append", lib().hca_paged_append(
+            k_new.data_ptr(), v_new.data_ptr(), s_new.data_ptr(), _ptr(q_start),
+            ctx_len.data_ptr(), S, N, ctypes.byref(cache), _stream(device)))
+
+
+def paged_prefill_workspace(S: int, N: int, device) -> torch.Tensor:
+    """Scratch for paged_prefill of N new tokens of S sequences (reusable across calls)."""
+    device = torch.device(device)
+    with _on(device):
+        return torch.empty((int(lib().hca_paged_prefill_workspace_size(S, N)),),
+                           dtype=torch.uint8, device=device)
+
+
+def paged_prefill(q: torch.Tensor, g: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                  s_new: torch.Tensor, q_start: torch.Tensor, ctx_len: torch.Tensor,
+                  wk: torch.Tensor, wv: torch.Tensor, ws: torch.Tensor, ck_pages: torch.Tensor,
+                  cv_pages: torch.Tensor, page_table: torch.Tensor, scale: Optional[float] = None,
+                  workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  vha=None) -> torch.Tensor:
+    """paged_append of a chunk, and the attention of its tokens over the cache.
+
+    q, g [N, 64, 512], packed like k_new -> out [N, 64, 512] bf16 (rows from
+    q_start[S] on are not written).  The other arguments are paged_append's;
+    `workspace` comes from paged_prefill_workspace; `vha` as for decode."""
+    device = wk.device
+    if q_start is None:
+        raise ValueError("paged_prefill needs q_start (paged_decode_step takes one token each)")
+    S, N = _check_chunk(k_new, v_new, s_new, q_start, ctx_len, device)
+    cache = _paged_cache(S, wk, wv, ws, ck_pages, cv_pages, page_table)
+    out, scale, down, up, r = _attend_args(q, g, out, vha, N, scale, device)
+    if N == 0:
+        return out
+    if workspace is None:
+        workspace = paged_prefill_workspace(S, N, device)
+    _check(workspace, "workspace", dtype=torch.uint8)
+    _check_on(device, (workspace, "workspace"))
+    with _on(device):
+        _ok("hca_paged_prefill", lib().hca_paged_prefill(
+            q.data_ptr(), g.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), s_new.data_ptr(),
+            q_start.data_ptr(), ctx_len.data_ptr(), S, N, HEADS, ctypes.c_float(scale), down, up, r,
+            ctypes.byref(cache), out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+            _stream(device)))
+    return out
+
+
+def paged_decode_workspace(S: int, device) -> torch.Tensor:
+    """A zero-filled workspace for paged_decode of up to S sequences (reusable across calls)."""
+    device = torch.device(device)
+    with _on(device):
+        return decode_workspace(S, device)
+
+
+def paged_decode(q: torch.Tensor, ck_pages: torch.Tensor, cv_pages: torch.Tensor,
+                 page_table: torch.Tensor, wk: torch.Tensor, wv: torch.Tensor,
+                 ctx_len: torch.Tensor, g: torch.Tensor, scale: Optional[float] = None,
+                 workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                 vha=None) -> torch.Tensor:
+    """decode over a paged cache: one query per sequence, q, g [S, 64, 512];
+    the cache (see paged_append) already holds its token.  A workspace passed
+    in comes from paged_decode_workspace."""
+    device = wk.device
+    S = ctx_len.shape[0]
+    _check(ctx_len, "ctx_len", (S,), dtype=torch.int32)
+    _check_on(device, (ctx_len, "ctx_len"))
+    cache = _paged_cache(S, wk, wv, None, ck_pages, cv_pages, page_table)
+    out, scale, down, up, r = _attend_args(q, g, out, vha, S, scale, device)
+    if workspace is None:
+        workspace = paged_decode_workspace(S, device)
+    _check(workspace, "workspace", dtype=torch.uint8)
+    _check_on(device, (workspace, "workspace"))
+    with _on(device):
+        _ok("hca_paged_decode", lib().hca_paged_decode(
+            q.data_ptr(), g.data_ptr(), ctx_len.data_ptr(), S, HEADS, ctypes.c_float(scale), down,
+            up, r, ctypes.byref(cache), out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+            _stream(device)))
+    return out
+
+
+def paged_decode_step(q: torch.Tensor, g: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                      s_new: torch.Tensor, ctx_len: torch.Tensor, wk: torch.Tensor,
+                      wv: torch.Tensor, ws: torch.Tensor, ck_pages: torch.Tensor,
+                      cv_pages: torch.Tensor, page_table: torch.Tensor,
+                      scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None, vha=None) -> torch.Tensor:
+    """One serving step: paged_append of one token per sequence (k_new, v_new
+    [S, 512]; s_new [S]), then paged_decode of their queries q, g [S, 64, 512]."""
+    device = wk.device
+    S, _ = _check_chunk(k_new, v_new, s_new, None, ctx_len, device)
+    cache = _paged_cache(S, wk, wv, ws, ck_pages, cv_pages, page_table)
+    out, scale, down, up, r = _attend_args(q, g, out, vha, S, scale, device)
+    if workspace is None:
+        workspace = paged_decode_workspace(S, device)
+    _check(workspace, "workspace", dtype=torch.uint8)
+    _check_on(device, (workspace, "workspace"))
+    with _on(device):
+        _ok("hca_paged_decode_step", lib().hca_paged_decode_step(
+            q.data_ptr(), g.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), s_new.data_ptr(),
+            ctx_len.data_ptr(), S, HEADS, ctypes.c_float(scale), down, up, r, ctypes.byref(cache),
+            out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(device)))
+    return out
+
+
+def _page_table(page_table, n_pages, ref, page_size: int) -> _PageTable:
+    if page_size not in PAGE_SIZES:
+        raise ValueError(f"pages must hold 16, 32, 64 or 128 entries, got {page_size}")
+    rows = n_pages.shape[0]
+    _check(n_pages, "n_pages", (rows,), dtype=torch.int32)
+    _check(ref, "ref", (ref.numel(),), dtype=torch.int32)
+    cols, stride = _check_table(page_table, rows)
+    _check_on(page_table.device, (n_pages, "n_pages"), (ref, "ref"))
+    return _PageTable(page_table.data_ptr(), stride, rows, cols, n_pages.data_ptr(),
+                      ref.data_ptr(), ref.numel(), page_size)
+
+
+def _page_arrays(arrays, items: int, what: str, device):
+    """Item arrays for the library: any dtype, contiguous, [items, ...]."""
+    out = (_PageArray * max(1, len(arrays)))()
+    for i, t in enumerate(arrays):
+        if not isinstance(t, torch.Tensor) or t.device != device:
+            raise ValueError(f"{what}[{i}] must be a tensor on {device}")
+        if not t.is_contiguous() or t.dim() < 2 or t.shape[0] != items:
+            raise ValueError(f"{what}[{i}] must be contiguous [{items}, ...], got {tuple(t.shape)}")
+        nbytes = t.numel() // items * t.element_size()
+        if nbytes < 16 or nbytes % 16:
+            raise ValueError(f"{what}[{i}]: items of {nbytes} bytes, a multiple of 16 is needed")
+        out[i] = _PageArray(t.data_ptr(), nbytes)
+    return out
+
+
+def _pages_workspace(workspace, rows, num_pages, n, device):
+    size = int(lib().hca_pages_workspace_size(rows, num_pages, n))
+    if workspace is None:
+        return torch.empty((size,), dtype=torch.uint8, device=device)
+    _check(workspace, "workspace", dtype=torch.uint8)
+    _check_on(device, (workspace, "workspace"))
+    return workspace
+
+
+def resize_pages(page_table: torch.Tensor, n_pages: torch.Tensor, ref: torch.Tensor,
+                 entries: torch.Tensor, page_size: int,
+                 workspace: Optional[torch.Tensor] = None) -> None:
+    """Give every row of the page table the pages of entries[r] entries, in place.
+
+    page_table [R, max_pages], n_pages [R], ref [num_pages], entries [R], all
+    int32 on the device.  0 frees a row, a negative number leaves it.  Rows
+    shrink first; rows that grow take the lowest free pages, row by row, while
+    there are any (n_pages[r] tells what row r has)."""
+    device = page_table.device
+    table = _page_table(page_table, n_pages, ref, page_size)
+    _check(entries, "entries", (table.rows,), dtype=torch.int32)
+    _check_on(device, (entries, "entries"))
+    with _on(device):
+        workspace = _pages_workspace(workspace, table.rows, table.num_pages, 0, device)
+        _ok("hca_pages_resize", lib().hca_pages_resize(
+            ctypes.byref(table), entries.data_ptr(), workspace.data_ptr(), workspace.numel(),
+            _stream(device)))
+
+
+def fork_pages(page_table: torch.Tensor, n_pages: torch.Tensor, ref: torch.Tensor,
+               parents: torch.Tensor, children: torch.Tensor, entries: torch.Tensor, pools,
+               page_size: int, rings=(), workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Branch sequences: the empty row children[i] becomes a copy of parents[i]
+    at entries[i] entries (parents, children, entries [n] int32).
+
+    Full pages are shared; the partly filled one is copied in every pool
+    ([num_pages, ...] tensors), and row parents[i] of every ring ([R, ...]) to
+    row children[i].  Returns ok [n] int32: 0 where no page was free (or the
+    pair was refused, which device_error() reports)."""
+    device = page_table.device
+    table = _page_table(page_table, n_pages, ref, page_size)
+    n = parents.shape[0]
+    for t, name in ((parents, "parents"), (children, "children"), (entries, "entries")):
+        _check(t, name, (n,), dtype=torch.int32)
+        _check_on(device, (t, name))
+    pool_arrays = _page_arrays(pools, table.num_pages, "pools", device)
+    ring_arrays = _page_arrays(rings, table.rows, "rings", device)
+    ok = torch.empty((n,), dtype=torch.int32, device=device)
+    if n == 0:
+        return ok
+    with _on(device):
+        workspace = _pages_workspace(workspace, table.rows, table.num_pages, n, device)
+        _ok("hca_pages_fork", lib().hca_pages_fork(
+            ctypes.byref(table), parents.data_ptr(), children.data_ptr(), entries.data_ptr(), n,
+            pool_arrays, len(pools), ring_arrays, len(rings), ok.data_ptr(), workspace.data_ptr(),
+            workspace.numel(), _stream(device)))
+    return ok
+
+
+def compact_pages(page_table: torch.Tensor, n_pages: torch.Tensor, ref: torch.Tensor, pools,
+                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Close up a pool: the pages in use take the lowest numbers, page_table,
+    ref and the contents of every pool ([num_pages, ...]) follow.  Returns the
+    number of pages in use ([1] int32 on the device); all others are free."""
+    device = page_table.device
+    table = _page_table(page_table, n_pages, ref, PAGE_SIZES[0])
+    arrays = _page_arrays(pools, table.num_pages, "pools", device)
+    live = torch.empty((1,), dtype=torch.int32, device=device)
+    with _on(device):
+        workspace = _pages_workspace(workspace, table.rows, table.num_pages, 0, device)
+        _ok("hca_pages_compact", lib().hca_pages_compact(
+            ctypes.byref(table), arrays, len(pools), live.data_ptr(), workspace.data_ptr(),
+            workspace.numel(), _stream(device)))
+    return live
+
+
+def copy_pages(arrays, src: torch.Tensor, dst: torch.Tensor,
+               workspace: Optional[torch.Tensor] = None) -> None:
+    """Copy item src[i] to item dst[i] of every array ([items, ...] tensors of
+    any dtype; src, dst [n] int32).  Pairs out of range, and all pairs whose
+    destination is named twice or is also a source, are left out and reported
+    by device_error()."""
+    if len(arrays) == 0:
+        return
+    n, items, device = src.shape[0], arrays[0].shape[0], arrays[0].device
+    for t, name in ((src, "src"), (dst, "dst")):
+        _check(t, name, (n,), dtype=torch.int32)
+        _check_on(device, (t, name))
+    item_arrays = _page_arrays(arrays, items, "arrays", device)
+    if n == 0:
+        return
+    with _on(device):
+        workspace = _pages_workspace(workspace, 1, items, n, device)
+        _ok("hca_pages_copy", lib().hca_pages_copy(
+            item_arrays, len(arrays), items, src.data_ptr(), dst.data_ptr(), n,
+            workspace.data_ptr(), workspace.numel(), _stream(device)))
 
 
 def device_error(device: Optional[torch.device] = None) -> Tuple[int, int]:

@@ -1,0 +1,326 @@
+// Appending ragged chunks of new tokens to a paged cache.
+//
+// The cache of sequence i is its ring (the newest 128 raw tokens, slot =
+// position mod 128) and the pages that its page table row names: entry j lies
+// in page table[i][j / P], slot j mod P.  A chunk brings the tokens
+// [q_start[i], q_start[i + 1]) of the packed inputs as the newest ones of
+// sequence i, at positions L0 .. L1 - 1 with L1 = ctx_len[i].
+//
+// entries_kernel: every block of 128 positions that the chunk completes,
+//   w = softmax(s), ck = sum w k, cv = sum w v ('BaiduがERNIE 5.5 Flash Baseを
+//   公開' §2.1), its tokens taken from the ring (positions before L0) and from
+//   the chunk.  Same thread layout and order of sums as the whole-sequence
+//   compressor, so the entries are bit-identical to it.  With kRaw it also
+//   lays the 127 tokens before the chunk, the chunk and 17 zero rows one after
+//   another in the workspace, where the attention of the chunk reads the raw
+//   windows of all its tokens as contiguous rows.
+// finish_kernel, launched behind it: the ring takes the newest tokens (it may
+//   only change once every entry has been formed), and the queries' lengths,
+//   table rows and window rows are written for the attention.
+//
+// Both move bytes only: 2 KB a token in (and out again with kRaw).
+#pragma once
+
+#include "compress.cuh"
+#include "hca_ptx.cuh"
+
+namespace hca {
+namespace paged {
+
+constexpr int kD = 512;
+constexpr int kBlk = 128;
+constexpr int kBack = 127;      // tokens before the chunk that its first window needs
+constexpr int kPad = 144;       // workspace rows of a sequence beyond its n tokens
+constexpr int kThreads = 128;
+constexpr int kUnitsExtra = 4;  // blocks that n + kPad rows can touch beyond n / 128
+
+struct Cache {
+  uint16_t* wk;        // [S, 128, 512]
+  uint16_t* wv;
+  uint16_t* ws;        // [S, 128]
+  uint16_t* ck;        // [pages, P, 512]
+  uint16_t* cv;
+  const int* table;    // row i at table + i * table_ld
+  long long table_ld;
+  int max_pages;       // columns of the table
+  int num_pages;
+  int page_shift;
+};
+
+struct Chunk {
+  const uint16_t* k;   // [N, 512]
+  const uint16_t* v;
+  const uint16_t* s;   // [N]
+  const int* q_start;  // [S + 1], null: one token a sequence
+  const int* ctx_len;  // [S]
+  int S, N;
+};
+
+struct Span {
+  int qs, n, L0, L1;   // first packed token, tokens, positions [L0, L1)
+};
+
+// Bounds of sequence i.  Offsets outside of 0 .. N, or falling, and lengths
+// below the number of tokens or above 2^30 are clamped and (by the one caller
+// that asks) reported.
+__device__ __forceinline__ Span span_of(const Chunk& c, int i, bool report) {
+  Span r;
+  const int a = c.q_start != nullptr ? c.q_start[i] : i;
+  const int b = c.q_start != nullptr ? c.q_start[i + 1] : i + 1;
+  const int L = c.ctx_len[i];
+  r.qs = min(max(a, 0), c.N);
+  r.n = max(min(max(b, 0), c.N) - r.qs, 0);
+  r.L1 = min(max(L, r.n), 1 << 30);
+  r.L0 = r.L1 - r.n;
+  if (report && (r.qs != a || r.qs + r.n != b || (r.L1 != L && r.n > 0)))
+    record_error(DEVERR_BAD_INPUT, 210);
+  return r;
+}
+
+// first workspace row of sequence i: position L0 - 127
+__device__ __forceinline__ int raw_base(const Span& sp, int i) { return sp.qs + kPad * i; }
+
+// Row of entry j of sequence i in the page pools, or -1 (reported) where the
+// table has no page for it.
+__device__ __forceinline__ long long entry_row(const Cache& c, int i, int j, unsigned where) {
+  const int col = j >> c.page_shift;
+  int pg = -1;
+  if (col < c.max_pages) pg = c.table[i * c.table_ld + col];
+  if (static_cast<unsigned>(pg) >= static_cast<unsigned>(c.num_pages)) {
+    if (threadIdx.x == 0) record_error(DEVERR_BAD_INPUT, where);
+    return -1;
+  }
+  return (static_cast<long long>(pg) << c.page_shift) + (j & ((1 << c.page_shift) - 1));
+}
+
+// Sequence of work unit u when sequence i owns the units from
+// floor(q_start[i] / 128) + 4 i on (at least as many as it can need): found by
+// counting, every thread a share of the offsets, without a prefix sum.
+__device__ __forceinline__ int unit_seq(const Chunk& c, int u, int* red) {
+  int cnt = 0;
+  for (int i = threadIdx.x; i < c.S; i += kThreads) {
+    const int qs = c.q_start != nullptr ? min(max(c.q_start[i], 0), c.N) : i;
+    cnt += (qs / kBlk + kUnitsExtra * i <= u) ? 1 : 0;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = cnt;
+  __syncthreads();
+  cnt = red[0] + red[1] + red[2] + red[3];
+  return max(cnt - 1, 0);
+}
+
+// grid.x = floor(N / 128) + 4 S units, grid.y = 8 (K/V x 4 channel quarters)
+template <bool kRaw>
+__global__ void __launch_bounds__(kThreads)
+    entries_kernel(const Chunk c, const Cache cache, uint16_t* __restrict__ raw_k,
+                   uint16_t* __restrict__ raw_v) {
+  __shared__ float w[kBlk];
+  __shared__ float red[2][4];
+  __shared__ int cnt[4];
+  __shared__ float part[8][kBlk + 4];
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int u = blockIdx.x;
+  const int which = blockIdx.y >> 2, quarter = blockIdx.y & 3;
+  const int i = unit_seq(c, u, cnt);
+  const Span sp = span_of(c, i, false);
+  const int ubase = sp.qs / kBlk + kUnitsExtra * i;
+  if (u < ubase || sp.n == 0) return;
+  // block b, positions p0 .. p0 + 127; the first block is that of position L0 - 127
+  const int b = ((sp.L0 - kBack + kBlk) >> 7) - 1 + (u - ubase);
+  const int p0 = b * kBlk;
+  if (p0 > sp.L1 + 16) return;
+  const bool completes = b >= 0 && p0 + kBlk <= sp.L1 && p0 + kBlk > sp.L0;
+  if (!kRaw && !completes) return;
+
+  if (completes) {   // within-block softmax of the scores (fp32)
+    const int p = p0 + tid;
+    const uint16_t sb = p < sp.L0 ? cache.ws[static_cast<size_t>(i) * kBlk + tid]
+                                  : c.s[static_cast<size_t>(sp.qs) + (p - sp.L0)];
+    const float sv = __uint_as_float(static_cast<uint32_t>(sb) << 16);
+    float m = warp_max(sv);
+    if ((tid & 31) == 0) red[0][warp] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    const float e = expf(sv - m);
+    float z = warp_sum(e);
+    if ((tid & 31) == 0) red[1][warp] = z;
+    __syncthreads();
+    z = red[1][0] + red[1][1] + red[1][2] + red[1][3];
+    w[tid] = e / z;
+    __syncthreads();
+  }
+
+  // thread (r, c): tokens r, r + 8, .. and channels 8 c .. 8 c + 7 of the quarter
+  const uint16_t* ring = (which ? cache.wv : cache.wk) + static_cast<size_t>(i) * kBlk * kD;
+  const uint16_t* fresh = (which ? c.v : c.k) + static_cast<size_t>(sp.qs) * kD;
+  uint16_t* raw = which ? raw_v : raw_k;
+  const int col = quarter * 128 + (tid & 15) * 8;
+  const int r = tid >> 4;
+  uint4 x[16];
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    const int p = p0 + q * 8 + r;
+    x[q] = make_uint4(0u, 0u, 0u, 0u);
+    if (p >= sp.L0) {
+      if (p < sp.L1)
+        x[q] = __ldg(reinterpret_cast<const uint4*>(fresh + static_cast<size_t>(p - sp.L0) * kD + col));
+    } else if (p >= max(0, sp.L0 - kBack)) {
+      x[q] = *reinterpret_cast<const uint4*>(ring + static_cast<size_t>(p & (kBlk - 1)) * kD + col);
+    }
+  }
+  if constexpr (kRaw) {
+    const long long row0 = static_cast<long long>(raw_base(sp, i)) + kBack - sp.L0;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const int p = p0 + q * 8 + r;
+      if (p >= sp.L0 - kBack && p <= sp.L1 + 16)
+        *reinterpret_cast<uint4*>(raw + (row0 + p) * kD + col) = x[q];
+    }
+  }
+  if (!completes) return;
+  float acc[8];
+#pragma unroll
+  for (int a = 0; a < 8; ++a) acc[a] = 0.f;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    const float wi = w[q * 8 + r];
+    const uint32_t uu[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      acc[2 * a] = fmaf(wi, bf16lo_to_f32(uu[a]), acc[2 * a]);
+      acc[2 * a + 1] = fmaf(wi, bf16hi_to_f32(uu[a]), acc[2 * a + 1]);
+    }
+  }
+#pragma unroll
+  for (int a = 0; a < 8; ++a) part[r][(tid & 15) * 8 + a] = acc[a];
+  __syncthreads();
+  float tot = 0.f;
+#pragma unroll
+  for (int rr = 0; rr < 8; ++rr) tot += part[rr][tid];
+  const long long row = entry_row(cache, i, b, 211);
+  if (row < 0) return;
+  __nv_bfloat16 hb = __float2bfloat16_rn(tot);
+  (which ? cache.cv : cache.ck)[row * kD + quarter * 128 + tid] = *reinterpret_cast<uint16_t*>(&hb);
+}
+
+// What the attention reads of each query (null pointers: append alone).
+struct Queries {
+  int* len;        // [N] context length of the query
+  int* row_of;     // [N] its page table row
+  int* win_row;    // [N] its first window row
+  int* count;      // queries in all
+  unsigned long long* gsync;   // the attention's grid barrier, reset here
+};
+
+constexpr int kFinishY = 8;     // CTAs of a sequence, 16 ring slots each
+constexpr int kFinishThreads = 256;
+
+// grid (S, kFinishY)
+__global__ void __launch_bounds__(kFinishThreads)
+    finish_kernel(const Chunk c, const Cache cache, const Queries qr) {
+  const int i = blockIdx.x, tid = threadIdx.x;
+  const Span sp = span_of(c, i, blockIdx.y == 0 && tid == 0);
+  if (qr.count != nullptr) {
+    const int base = raw_base(sp, i);
+    for (int r = blockIdx.y * kFinishThreads + tid; r < sp.n; r += kFinishY * kFinishThreads) {
+      qr.len[sp.qs + r] = sp.L0 + r + 1;
+      qr.row_of[sp.qs + r] = i;
+      qr.win_row[sp.qs + r] = base + r;
+    }
+    if (i == 0 && blockIdx.y == 0 && tid == 0) {
+      *qr.count = min(max(c.q_start[c.S], 0), c.N);
+      *qr.gsync = 0ull;
+    }
+  }
+  constexpr int kSlots = kBlk / kFinishY;
+  // 16 slots x (K, V) x 64 chunks of 16 bytes
+#pragma unroll
+  for (int q = 0; q < kSlots * 2 * 64 / kFinishThreads; ++q) {
+    const int idx = q * kFinishThreads + tid;
+    const int slot = blockIdx.y * kSlots + (idx >> 7), which = (idx >> 6) & 1, col = (idx & 63) * 8;
+    const int p = sp.L1 - 1 - ((sp.L1 - 1 - slot) & (kBlk - 1));   // newest position of the slot
+    if (sp.n > 0 && p >= sp.L0) {
+      const size_t tok = static_cast<size_t>(sp.qs) + (p - sp.L0);
+      const size_t dst = (static_cast<size_t>(i) * kBlk + slot) * kD + col;
+      *reinterpret_cast<uint4*>((which ? cache.wv : cache.wk) + dst) =
+          __ldg(reinterpret_cast<const uint4*>((which ? c.v : c.k) + tok * kD + col));
+      if (col == 0 && which == 0) cache.ws[static_cast<size_t>(i) * kBlk + slot] = c.s[tok];
+    }
+  }
+}
+
+// One token a sequence (ring write and, where a block completes, its entry) in
+// one launch: grid (S, 8), CTA (i, y) = (K or V, channel quarter) of sequence i,
+// 128 threads.  Latency-bound.  Each CTA reads and writes its own channels of
+// the ring; the newest row and score are taken from the inputs, so no CTA
+// waits for another's ring write.
+__global__ void __launch_bounds__(kThreads) step_kernel(const Chunk c, const Cache cache) {
+  __shared__ float w[kBlk];
+  __shared__ float red[2][4];
+  __shared__ float part[8][kBlk + 4];
+  const int i = blockIdx.x, tid = threadIdx.x, warp = tid >> 5;
+  const int which = blockIdx.y >> 2, quarter = blockIdx.y & 3;
+  const int L = c.ctx_len[i];
+  if (L < 1) {
+    if (tid == 0 && blockIdx.y == 0) record_error(DEVERR_BAD_INPUT, 212);
+    return;
+  }
+  const int slot = (L - 1) & (kBlk - 1);
+  uint16_t* ring = (which ? cache.wv : cache.wk) + static_cast<size_t>(i) * kBlk * kD;
+  const uint16_t* fresh = (which ? c.v : c.k) + static_cast<size_t>(i) * kD;
+  const int col = quarter * 128 + (tid & 15) * 8;
+  const int r = tid >> 4;
+  if (tid < 16)
+    *reinterpret_cast<uint4*>(ring + static_cast<size_t>(slot) * kD + col) =
+        __ldg(reinterpret_cast<const uint4*>(fresh + col));
+  if (tid == 32 && blockIdx.y == 0) cache.ws[static_cast<size_t>(i) * kBlk + slot] = c.s[i];
+  if ((L & (kBlk - 1)) != 0) return;
+  // the block L / 128 - 1 is the ring, its newest row in slot 127
+  const uint16_t sb = tid == kBlk - 1 ? c.s[i] : cache.ws[static_cast<size_t>(i) * kBlk + tid];
+  uint4 x[16];
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    const int t = q * 8 + r;
+    x[q] = t == kBlk - 1 ? __ldg(reinterpret_cast<const uint4*>(fresh + col))
+                         : *reinterpret_cast<const uint4*>(ring + static_cast<size_t>(t) * kD + col);
+  }
+  const float sv = __uint_as_float(static_cast<uint32_t>(sb) << 16);
+  float m = warp_max(sv);
+  if ((tid & 31) == 0) red[0][warp] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  const float e = expf(sv - m);
+  float z = warp_sum(e);
+  if ((tid & 31) == 0) red[1][warp] = z;
+  __syncthreads();
+  z = red[1][0] + red[1][1] + red[1][2] + red[1][3];
+  w[tid] = e / z;
+  __syncthreads();
+  float acc[8];
+#pragma unroll
+  for (int a = 0; a < 8; ++a) acc[a] = 0.f;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    const float wi = w[q * 8 + r];
+    const uint32_t uu[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      acc[2 * a] = fmaf(wi, bf16lo_to_f32(uu[a]), acc[2 * a]);
+      acc[2 * a + 1] = fmaf(wi, bf16hi_to_f32(uu[a]), acc[2 * a + 1]);
+    }
+  }
+#pragma unroll
+  for (int a = 0; a < 8; ++a) part[r][(tid & 15) * 8 + a] = acc[a];
+  __syncthreads();
+  float tot = 0.f;
+#pragma unroll
+  for (int rr = 0; rr < 8; ++rr) tot += part[rr][tid];
+  const long long row = entry_row(cache, i, L / kBlk - 1, 213);
+  if (row < 0) return;
+  __nv_bfloat16 hb = __float2bfloat16_rn(tot);
+  (which ? cache.cv : cache.ck)[row * kD + quarter * 128 + tid] = *reinterpret_cast<uint16_t*>(&hb);
+}
+
+}  // namespace paged
+}  // namespace hca

@@ -1,0 +1,437 @@
+// Host side of the paged cache: argument checks, maps and launches of the
+// calls that include/hca.h declares under "Paged cache".  Part of the one
+// translation unit of hca_lib.cu, whose helpers it uses.
+#pragma once
+
+namespace {
+
+// log2 of a page size the kernels take (16, 32, 64 or 128 entries), or -1
+int page_shift_of(int page_size) {
+  for (int s = 4; s <= 7; ++s)
+    if (page_size == 1 << s) return s;
+  return -1;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+// Checks what every call on a paged cache shares and fills `c`.
+hca_status_t paged_cache(hca::paged::Cache& c, const hca_paged_cache_t* p, int S, bool ring_scores) {
+  if (p == nullptr) return HCA_ERR_INVALID_ARG;
+  if (p->num_pages < 0 || p->max_pages < 0 || p->table_stride < p->max_pages)
+    return HCA_ERR_INVALID_ARG;
+  const int shift = page_shift_of(p->page_size);
+  if (shift < 0) return HCA_ERR_UNSUPPORTED;
+  if (p->wk == nullptr || p->wv == nullptr || !aligned16(p->wk) || !aligned16(p->wv) ||
+      (ring_scores && p->ws == nullptr))
+    return HCA_ERR_INVALID_ARG;
+  if (p->num_pages > 0 && (p->ck == nullptr || p->cv == nullptr || !aligned16(p->ck) ||
+                           !aligned16(p->cv)))
+    return HCA_ERR_INVALID_ARG;
+  if (p->max_pages > 0 && (p->page_table == nullptr || !aligned4(p->page_table)))
+    return HCA_ERR_INVALID_ARG;
+  // entry numbers and ring rows are 32-bit
+  if (static_cast<long long>(p->max_pages) * p->page_size > 0x7fffffffLL / HCA_BLOCK ||
+      S > 0x7fffffff / HCA_BLOCK)
+    return HCA_ERR_UNSUPPORTED;
+  c.wk = p->wk;
+  c.wv = p->wv;
+  c.ws = p->ws;
+  c.ck = p->ck;
+  c.cv = p->cv;
+  c.table = p->page_table;
+  c.table_ld = p->table_stride;
+  c.max_pages = p->max_pages;
+  c.num_pages = p->num_pages;
+  c.page_shift = shift;
+  return HCA_OK;
+}
+
+hca_status_t chunk_args(hca::paged::Chunk& c, const hca_bf16* k_new, const hca_bf16* v_new,
+                        const hca_bf16* s_new, const int32_t* q_start, const int32_t* ctx_len,
+                        int S, int N) {
+  if (S < 1 || N < 0 || k_new == nullptr || v_new == nullptr || s_new == nullptr ||
+      ctx_len == nullptr || !aligned16(k_new) || !aligned16(v_new) || !aligned4(ctx_len) ||
+      !aligned4(q_start))
+    return HCA_ERR_INVALID_ARG;
+  c = {k_new, v_new, s_new, q_start, ctx_len, S, N};
+  return HCA_OK;
+}
+
+// grid.x of entries_kernel: the units of all sequences
+long long entry_units(int S, int N) {
+  return N / hca::paged::kBlk + static_cast<long long>(hca::paged::kUnitsExtra) * S;
+}
+
+// Decode parameters over a paged cache; `rows`: queries (and their maps' rows).
+hca_status_t paged_attend(const hca::paged::Cache& c, const hca_bf16* q, const hca_bf16* g,
+                          hca_bf16* out, const hca_bf16* wk, const hca_bf16* wv,
+                          uint64_t win_rows, hca::decode::Params& prm, uint8_t* ws,
+                          cudaStream_t stream) {
+  namespace D = hca::decode;
+  const int sms = device_sms();
+  if (sms <= 0) return HCA_ERR_CUDA;
+  const int slots = sms + prm.S;
+  prm.max_nc = c.max_pages << c.page_shift;
+  prm.gsync = reinterpret_cast<unsigned long long*>(ws);
+  prm.ws_o = reinterpret_cast<uint16_t*>(ws + 256);
+  prm.ws_ml = reinterpret_cast<float*>(ws + 256 + D::ws_o_bytes(slots));
+  prm.seq_tile = reinterpret_cast<long long*>(ws + 256 + align256(D::ws_bytes(slots)));
+  prm.g = g;
+  prm.out = out;
+  prm.table = c.table;
+  prm.table_ld = c.table_ld;
+  prm.num_pages = c.num_pages;
+  prm.page_shift = c.page_shift;
+  D::Maps maps;
+  const uint32_t box = 1u << c.page_shift;
+  bool ok = make_map4(&maps.q, q, static_cast<uint64_t>(prm.S) * HCA_NUM_HEADS, 1, 64, 8) &&
+            make_map4(&maps.wk, wk, win_rows, 1, 128, 2) &&
+            make_map4(&maps.wv, wv, win_rows, 1, 128, 2);
+  if (ok && c.num_pages > 0) {
+    ok = make_map4(&maps.ck, c.ck, box, c.num_pages, box, 1) &&
+         make_map4(&maps.cv, c.cv, box, c.num_pages, box, 1);
+  } else if (ok) {   // no page exists: every box falls outside of these
+    prm.num_pages = 0;
+    prm.max_nc = 0;
+    maps.ck = maps.wk;
+    maps.cv = maps.wv;
+  }
+  if (!ok) return HCA_ERR_CUDA;
+  if (launch_decode<false, true>(maps, prm, sms, stream) != cudaSuccess) return HCA_ERR_CUDA;
+  return launch_status();
+}
+
+// What an attention call shares beside its cache.
+hca_status_t attend_args(const hca_bf16* q, const hca_bf16* g, const hca_bf16* out, int H,
+                         float scale, const hca_bf16* vha_down, const hca_bf16* vha_up,
+                         int vha_rank, const void* ws) {
+  if (H != HCA_NUM_HEADS) return HCA_ERR_UNSUPPORTED;
+  if (!scale_ok(scale) || q == nullptr || g == nullptr || out == nullptr || ws == nullptr)
+    return HCA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(g) || !aligned16(out)) return HCA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return HCA_ERR_INVALID_ARG;
+  if (vha_rank < 0 || vha_rank > HCA_NUM_HEADS ||
+      (vha_rank > 0 && (vha_down == nullptr || vha_up == nullptr)))
+    return HCA_ERR_INVALID_ARG;
+  return HCA_OK;
+}
+
+struct PagedPrefillLayout {
+  size_t decode, len, row_of, win_row, count, raw_k, raw_v, total;
+};
+
+PagedPrefillLayout paged_prefill_layout(int S, int N) {
+  PagedPrefillLayout L = {};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align256(off + bytes);
+    return at;
+  };
+  L.decode = take(hca_decode_workspace_size(N));
+  L.len = take(static_cast<size_t>(N) * 4);
+  L.row_of = take(static_cast<size_t>(N) * 4);
+  L.win_row = take(static_cast<size_t>(N) * 4);
+  L.count = take(4);
+  const size_t raw = (static_cast<size_t>(N) + static_cast<size_t>(hca::paged::kPad) * S) *
+                     HCA_HEAD_DIM * 2;
+  L.raw_k = take(raw);
+  L.raw_v = take(raw);
+  L.total = off;
+  return L;
+}
+
+}  // namespace
+
+extern "C" {
+
+hca_status_t hca_paged_append(const hca_bf16* k_new, const hca_bf16* v_new, const hca_bf16* s_new,
+                              const int32_t* q_start, const int32_t* ctx_len, int S, int N,
+                              const hca_paged_cache_t* cache, hca_stream_t stream) {
+  namespace G = hca::paged;
+  G::Cache c;
+  G::Chunk ch;
+  hca_status_t st = chunk_args(ch, k_new, v_new, s_new, q_start, ctx_len, S, N);
+  if (st != HCA_OK) return st;
+  if (q_start == nullptr && N != S) return HCA_ERR_INVALID_ARG;
+  st = paged_cache(c, cache, S, true);
+  if (st != HCA_OK) return st;
+  if (N == 0) return HCA_OK;
+  if (q_start == nullptr) {
+    G::step_kernel<<<dim3(S, 8), G::kThreads, 0, stream>>>(ch, c);
+    return launch_status();
+  }
+  const long long units = entry_units(S, N);
+  if (units > 0x7fffffffLL) return HCA_ERR_UNSUPPORTED;
+  G::entries_kernel<false>
+      <<<dim3(static_cast<unsigned>(units), 8), G::kThreads, 0, stream>>>(ch, c, nullptr, nullptr);
+  G::finish_kernel<<<dim3(S, G::kFinishY), G::kFinishThreads, 0, stream>>>(ch, c, G::Queries{});
+  return launch_status();
+}
+
+size_t hca_paged_prefill_workspace_size(int S, int N) {
+  if (S < 1 || N < 1 || device_sms() <= 0) return 0;
+  return paged_prefill_layout(S, N).total;
+}
+
+hca_status_t hca_paged_prefill(const hca_bf16* q, const hca_bf16* g, const hca_bf16* k_new,
+                               const hca_bf16* v_new, const hca_bf16* s_new,
+                               const int32_t* q_start, const int32_t* ctx_len, int S, int N, int H,
+                               float scale, const hca_bf16* vha_down, const hca_bf16* vha_up,
+                               int vha_rank, const hca_paged_cache_t* cache, hca_bf16* out,
+                               void* ws, size_t ws_bytes, hca_stream_t stream) {
+  namespace G = hca::paged;
+  G::Cache c;
+  G::Chunk ch;
+  hca_status_t st = attend_args(q, g, out, H, scale, vha_down, vha_up, vha_rank, ws);
+  if (st != HCA_OK) return st;
+  st = chunk_args(ch, k_new, v_new, s_new, q_start, ctx_len, S, N);
+  if (st != HCA_OK) return st;
+  if (q_start == nullptr) return HCA_ERR_INVALID_ARG;
+  st = paged_cache(c, cache, S, true);
+  if (st != HCA_OK) return st;
+  if (N == 0) return HCA_OK;
+  const long long units = entry_units(S, N);
+  if (S > 65535 || static_cast<long long>(N) + static_cast<long long>(G::kPad) * S >
+                       0x7fffffffLL / HCA_NUM_HEADS)
+    return HCA_ERR_UNSUPPORTED;
+  const PagedPrefillLayout L = paged_prefill_layout(S, N);
+  if (ws_bytes < L.total) return HCA_ERR_INVALID_ARG;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  uint16_t* raw_k = reinterpret_cast<uint16_t*>(w + L.raw_k);
+  uint16_t* raw_v = reinterpret_cast<uint16_t*>(w + L.raw_v);
+  G::Queries qr;
+  qr.len = reinterpret_cast<int*>(w + L.len);
+  qr.row_of = reinterpret_cast<int*>(w + L.row_of);
+  qr.win_row = reinterpret_cast<int*>(w + L.win_row);
+  qr.count = reinterpret_cast<int*>(w + L.count);
+  qr.gsync = reinterpret_cast<unsigned long long*>(w + L.decode);
+  G::entries_kernel<true>
+      <<<dim3(static_cast<unsigned>(units), 8), G::kThreads, 0, stream>>>(ch, c, raw_k, raw_v);
+  G::finish_kernel<<<dim3(S, G::kFinishY), G::kFinishThreads, 0, stream>>>(ch, c, qr);
+  hca::decode::Params prm = {};
+  prm.ctx_len = qr.len;
+  prm.S = N;
+  prm.scale_log2 = scale * 1.4426950408889634f;
+  prm.vha_down = vha_down;
+  prm.vha_up = vha_up;
+  prm.vha_rank = vha_rank;
+  prm.row_of = qr.row_of;
+  prm.win_row = qr.win_row;
+  prm.count = qr.count;
+  return paged_attend(c, q, g, out, raw_k, raw_v,
+                      static_cast<uint64_t>(N) + static_cast<uint64_t>(G::kPad) * S, prm,
+                      w + L.decode, stream);
+}
+
+hca_status_t hca_paged_decode(const hca_bf16* q, const hca_bf16* g, const int32_t* ctx_len, int S,
+                              int H, float scale, const hca_bf16* vha_down,
+                              const hca_bf16* vha_up, int vha_rank,
+                              const hca_paged_cache_t* cache, hca_bf16* out, void* ws,
+                              size_t ws_bytes, hca_stream_t stream) {
+  hca::paged::Cache c;
+  hca_status_t st = attend_args(q, g, out, H, scale, vha_down, vha_up, vha_rank, ws);
+  if (st != HCA_OK) return st;
+  if (S < 1 || ctx_len == nullptr || !aligned4(ctx_len)) return HCA_ERR_INVALID_ARG;
+  if (S > 65535) return HCA_ERR_UNSUPPORTED;
+  st = paged_cache(c, cache, S, false);
+  if (st != HCA_OK) return st;
+  if (ws_bytes < hca_decode_workspace_size(S)) return HCA_ERR_INVALID_ARG;
+  hca::decode::Params prm = {};
+  prm.ctx_len = ctx_len;
+  prm.S = S;
+  prm.scale_log2 = scale * 1.4426950408889634f;
+  prm.vha_down = vha_down;
+  prm.vha_up = vha_up;
+  prm.vha_rank = vha_rank;
+  return paged_attend(c, q, g, out, c.wk, c.wv, static_cast<uint64_t>(S) * HCA_WINDOW, prm,
+                      static_cast<uint8_t*>(ws), stream);
+}
+
+hca_status_t hca_paged_decode_step(const hca_bf16* q, const hca_bf16* g, const hca_bf16* k_new,
+                                   const hca_bf16* v_new, const hca_bf16* s_new,
+                                   const int32_t* ctx_len, int S, int H, float scale,
+                                   const hca_bf16* vha_down, const hca_bf16* vha_up, int vha_rank,
+                                   const hca_paged_cache_t* cache, hca_bf16* out, void* ws,
+                                   size_t ws_bytes, hca_stream_t stream) {
+  // validate both halves before launching either
+  hca::paged::Cache c;
+  hca_status_t st = attend_args(q, g, out, H, scale, vha_down, vha_up, vha_rank, ws);
+  if (st != HCA_OK) return st;
+  if (S < 1) return HCA_ERR_INVALID_ARG;
+  if (S > 65535) return HCA_ERR_UNSUPPORTED;
+  st = paged_cache(c, cache, S, true);
+  if (st != HCA_OK) return st;
+  if (ws_bytes < hca_decode_workspace_size(S)) return HCA_ERR_INVALID_ARG;
+  st = hca_paged_append(k_new, v_new, s_new, nullptr, ctx_len, S, S, cache, stream);
+  if (st != HCA_OK) return st;
+  return hca_paged_decode(q, g, ctx_len, S, H, scale, vha_down, vha_up, vha_rank, cache, out, ws,
+                          ws_bytes, stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Page management
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int kMaxForks = 8192;
+
+hca_status_t page_rows(hca::pages::Table& t, const hca_page_table_t* p) {
+  if (p == nullptr || p->rows < 1 || p->max_pages < 1 || p->num_pages < 1 ||
+      p->table_stride < p->max_pages)
+    return HCA_ERR_INVALID_ARG;
+  const int shift = page_shift_of(p->page_size);
+  if (shift < 0) return HCA_ERR_UNSUPPORTED;
+  if (p->page_table == nullptr || p->n_pages == nullptr || p->ref == nullptr ||
+      !aligned4(p->page_table) || !aligned4(p->n_pages) || !aligned4(p->ref))
+    return HCA_ERR_INVALID_ARG;
+  t = {p->page_table, p->table_stride, p->rows, p->max_pages, p->n_pages, p->ref, p->num_pages,
+       shift};
+  return HCA_OK;
+}
+
+// Adds `n` arrays with the given lists to `m`.
+hca_status_t move_arrays(hca::pages::Move& m, const hca_page_array_t* arrays, int n, const int* src,
+                         const int* dst) {
+  if (n < 0 || (n > 0 && arrays == nullptr)) return HCA_ERR_INVALID_ARG;
+  if (m.arrays + n > hca::pages::kMaxArrays) return HCA_ERR_UNSUPPORTED;
+  for (int i = 0; i < n; ++i) {
+    if (arrays[i].data == nullptr || !aligned16(arrays[i].data) || arrays[i].item_bytes < 16 ||
+        arrays[i].item_bytes % 16 != 0)
+      return HCA_ERR_INVALID_ARG;
+    m.a[m.arrays++] = {static_cast<uint8_t*>(arrays[i].data), arrays[i].item_bytes, src, dst};
+  }
+  return HCA_OK;
+}
+
+hca_status_t launch_move(const hca::pages::Move& m, cudaStream_t stream) {
+  namespace P = hca::pages;
+  if (m.n < 1 || (m.arrays == 0 && m.table == nullptr)) return launch_status();
+  const int sms = device_sms();
+  if (sms <= 0) return HCA_ERR_CUDA;
+  long long units = 0;
+  for (int i = 0; i < m.arrays; ++i) units += (m.a[i].bytes + P::kUnit - 1) / P::kUnit * m.n;
+  const long long table = (static_cast<long long>(m.rows) * m.max_pages + 1023) / 1024;
+  units = units > table ? units : table;
+  const long long most = 8LL * sms;
+  P::move_kernel<<<static_cast<unsigned>(units < most ? units : most), P::kMoveThreads, 0,
+                   stream>>>(m);
+  return launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t hca_pages_workspace_size(int rows, int num_pages, int n) {
+  if (rows < 1 || num_pages < 1 || n < 0) return 0;
+  // the largest of: resize (free list, prefix), fork (four lists), compact (two half lists,
+  // remap, count), copy (marks, two lists)
+  const size_t pages = num_pages, list = n;
+  const size_t resize = pages + rows + 1, fork = 4 * list, compact = 2 * (pages / 2 + 1) + pages + 1,
+               copy = pages + 2 * list;
+  size_t most = resize;
+  for (const size_t x : {fork, compact, copy}) most = x > most ? x : most;
+  return align256(most * 4);
+}
+
+hca_status_t hca_pages_resize(const hca_page_table_t* table, const int32_t* entries, void* ws,
+                              size_t ws_bytes, hca_stream_t stream) {
+  namespace P = hca::pages;
+  P::Table t;
+  const hca_status_t st = page_rows(t, table);
+  if (st != HCA_OK) return st;
+  if (entries == nullptr || ws == nullptr || !aligned4(entries) || !aligned16(ws) ||
+      ws_bytes < hca_pages_workspace_size(t.rows, t.num_pages, 0))
+    return HCA_ERR_INVALID_ARG;
+  int* free_list = static_cast<int*>(ws);
+  P::resize_kernel<<<1, P::kPlanThreads, 0, stream>>>(t, entries, free_list,
+                                                      free_list + t.num_pages);
+  return launch_status();
+}
+
+hca_status_t hca_pages_fork(const hca_page_table_t* table, const int32_t* parents,
+                            const int32_t* children, const int32_t* entries, int n,
+                            const hca_page_array_t* pools, int n_pools,
+                            const hca_page_array_t* rings, int n_rings, int32_t* ok, void* ws,
+                            size_t ws_bytes, hca_stream_t stream) {
+  namespace P = hca::pages;
+  P::Table t;
+  hca_status_t st = page_rows(t, table);
+  if (st != HCA_OK) return st;
+  if (n < 0 || parents == nullptr || children == nullptr || entries == nullptr || ok == nullptr ||
+      ws == nullptr || !aligned4(parents) || !aligned4(children) || !aligned4(entries) ||
+      !aligned4(ok) || !aligned16(ws) ||
+      ws_bytes < hca_pages_workspace_size(t.rows, t.num_pages, n))
+    return HCA_ERR_INVALID_ARG;
+  if (n > kMaxForks) return HCA_ERR_UNSUPPORTED;
+  int* src = static_cast<int*>(ws);
+  int *dst = src + n, *rsrc = src + 2 * n, *rdst = src + 3 * n;
+  P::Move m = {};
+  m.n = n;
+  st = move_arrays(m, pools, n_pools, src, dst);
+  if (st == HCA_OK) st = move_arrays(m, rings, n_rings, rsrc, rdst);
+  if (st != HCA_OK) return st;
+  if (n == 0) return HCA_OK;
+  P::fork_kernel<<<1, P::kPlanThreads, 0, stream>>>(t, parents, children, entries, n, ok, src, dst,
+                                                    rsrc, rdst);
+  st = launch_status();
+  return st == HCA_OK ? launch_move(m, stream) : st;
+}
+
+hca_status_t hca_pages_compact(const hca_page_table_t* table, const hca_page_array_t* pools,
+                               int n_pools, int32_t* live, void* ws, size_t ws_bytes,
+                               hca_stream_t stream) {
+  namespace P = hca::pages;
+  P::Table t;
+  hca_status_t st = page_rows(t, table);
+  if (st != HCA_OK) return st;
+  if (live == nullptr || ws == nullptr || !aligned4(live) || !aligned16(ws) ||
+      ws_bytes < hca_pages_workspace_size(t.rows, t.num_pages, 0))
+    return HCA_ERR_INVALID_ARG;
+  const int half = t.num_pages / 2 + 1;
+  int* src = static_cast<int*>(ws);
+  int *dst = src + half, *remap = src + 2 * half, *count = remap + t.num_pages;
+  P::Move m = {};
+  m.n = t.num_pages / 2;
+  m.count = count;
+  m.table = t.table;
+  m.table_ld = t.ld;
+  m.rows = t.rows;
+  m.max_pages = t.max_pages;
+  m.remap = remap;
+  m.live = live;
+  m.num_pages = t.num_pages;
+  st = move_arrays(m, pools, n_pools, src, dst);
+  if (st != HCA_OK) return st;
+  P::compact_kernel<<<1, P::kPlanThreads, 0, stream>>>(t.ref, t.num_pages, src, dst, count, remap,
+                                                       live);
+  st = launch_status();
+  return st == HCA_OK ? launch_move(m, stream) : st;
+}
+
+hca_status_t hca_pages_copy(const hca_page_array_t* arrays, int n_arrays, int items,
+                            const int32_t* src, const int32_t* dst, int n, void* ws,
+                            size_t ws_bytes, hca_stream_t stream) {
+  namespace P = hca::pages;
+  if (items < 1 || n < 0 || n >= 1 << 30 || src == nullptr || dst == nullptr || ws == nullptr ||
+      !aligned4(src) || !aligned4(dst) || !aligned16(ws) ||
+      ws_bytes < hca_pages_workspace_size(1, items, n))
+    return HCA_ERR_INVALID_ARG;
+  int* mark = static_cast<int*>(ws);
+  int *from = mark + items, *to = from + n;
+  P::Move m = {};
+  m.n = n;
+  const hca_status_t st = move_arrays(m, arrays, n_arrays, from, to);
+  if (st != HCA_OK) return st;
+  if (n == 0) return HCA_OK;
+  if (cudaMemsetAsync(mark, 0, static_cast<size_t>(items) * 4, stream) != cudaSuccess)
+    return HCA_ERR_CUDA;
+  P::check_kernel<<<1, P::kPlanThreads, 0, stream>>>(src, dst, n, items, mark, from, to);
+  return launch_move(m, stream);
+}
+
+}  // extern "C"

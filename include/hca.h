@@ -334,6 +334,195 @@ hca_status_t hca_decode_e4m3(const hca_bf16* q, const uint8_t* ck, const float* 
                              int S, int H, float scale, void* ws, size_t ws_bytes, hca_bf16* out,
                              hca_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged cache
+ *
+ * The compressed entries of many sequences share one pool of pages, each of
+ * `page_size` entries (16, 32, 64 or 128; an entry stands for 128 tokens).
+ * Entry j of sequence i is row j % page_size of page
+ * page_table[i][j / page_size].  The raw window of sequence i is row i of the
+ * rings, as for hca_decode.  Rows of the pool behind a sequence's last entry,
+ * ring slots without a token, other sequences' pages and table columns that no
+ * entry needs may hold anything, NaN included.  A page number outside of the
+ * pool where one is needed reads as zero rows (a write there is left out) and
+ * is reported by hca_get_device_error() as HCA_ERR_DEVICE_INPUT.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  hca_bf16* wk; /* [S, 128, 512] raw window rings (slot = position mod 128)    */
+  hca_bf16* wv;
+  hca_bf16* ws; /* [S, 128] their scores (not read by hca_paged_decode)        */
+  hca_bf16* ck; /* [num_pages, page_size, 512] entry pools                     */
+  hca_bf16* cv;
+  const int32_t* page_table; /* row i at page_table + i * table_stride         */
+  long long table_stride;    /* >= max_pages                                   */
+  int max_pages;             /* columns                                        */
+  int num_pages;
+  int page_size;
+} hca_paged_cache_t;
+
+/*
+ * hca_paged_append — append a chunk of new tokens per sequence to a paged cache
+ *   (hca_cache_append for any number of tokens; same sources).
+ *   Sequence i brings the tokens q_start[i] .. q_start[i + 1] - 1 (possibly
+ *   none) of the packed inputs; ctx_len[i] counts them, so they sit at
+ *   positions ctx_len[i] - n .. ctx_len[i] - 1.  Every block of 128 positions
+ *   that they complete becomes an entry in its page, bit-identical to
+ *   hca_compress of the whole sequence; the ring takes the newest tokens.
+ *   q_start NULL: one token per sequence (N = S), in one launch instead of two.
+ * Layout:  k_new, v_new [N, 512] bf16;  s_new [N] bf16;  q_start [S + 1] and
+ *          ctx_len [S] int32 on the device.  A page that is written must not
+ *          be shared with another sequence (hca_pages_fork sees to that).
+ * Errors:  HCA_ERR_INVALID_ARG for S < 1, N < 0, a NULL or misaligned pointer,
+ *          q_start NULL with N != S; HCA_ERR_UNSUPPORTED for another page size
+ *          or a table of more than 2^31 / 128 entries a row.  On the device:
+ *          offsets that fall or leave 0 .. N, and lengths below the tokens
+ *          brought or above 2^30, are clamped and reported.
+ */
+hca_status_t hca_paged_append(const hca_bf16* k_new, const hca_bf16* v_new, const hca_bf16* s_new,
+                              const int32_t* q_start, const int32_t* ctx_len, int S, int N,
+                              const hca_paged_cache_t* cache, hca_stream_t stream);
+
+/*
+ * hca_paged_prefill_workspace_size — bytes of scratch hca_paged_prefill needs
+ * for S sequences with N new tokens in all.  Returns 0 for S < 1 or N < 1.
+ */
+size_t hca_paged_prefill_workspace_size(int S, int N);
+
+/*
+ * hca_paged_prefill — hca_paged_append, and the attention of every new token
+ *   over its sequence (chunked prefill, drafts of several tokens, mixed
+ *   batches).  For the token at position t:
+ *     keys = [entries 0 .. nc(t) - 1 ; raw keys max(0, t - 127) .. t]
+ *     out  = sigmoid(g) * softmax(scale * keys . q) . values
+ *   with nc(t) as above, then (vha_rank > 0) the head mix of hca_decode_vha.
+ * Layout:  q, g, out [N, H, 512] bf16 (H = 64), packed as k_new; rows from
+ *          q_start[S] on are not written.  vha_down, vha_up [64, vha_rank]
+ *          bf16 (vha_rank = 0: none, may be NULL).  ws: at least
+ *          hca_paged_prefill_workspace_size(S, N) bytes, 256-byte aligned,
+ *          needs no initialisation; calls that overlap need one each.
+ *          A token's values must be finite: one that is not may also reach the
+ *          outputs of up to 16 positions before it in its sequence, and
+ *          nothing else's.
+ * Errors:  those of hca_paged_append (q_start is required), of hca_decode_vha,
+ *          and HCA_ERR_UNSUPPORTED for S > 65535 or (N + 144 S) * 64 >= 2^31.
+ */
+hca_status_t hca_paged_prefill(const hca_bf16* q, const hca_bf16* g, const hca_bf16* k_new,
+                               const hca_bf16* v_new, const hca_bf16* s_new,
+                               const int32_t* q_start, const int32_t* ctx_len, int S, int N, int H,
+                               float scale, const hca_bf16* vha_down, const hca_bf16* vha_up,
+                               int vha_rank, const hca_paged_cache_t* cache, hca_bf16* out,
+                               void* ws, size_t ws_bytes, hca_stream_t stream);
+
+/*
+ * hca_paged_decode — hca_decode (vha_rank > 0: hca_decode_vha) over a paged
+ *   cache: one query per sequence, the cache already holding its token.
+ *   Reads the cache only.  q, g, out [S, 64, 512]; ws as for hca_decode.
+ * Errors:  as hca_decode_vha and hca_paged_append.
+ */
+hca_status_t hca_paged_decode(const hca_bf16* q, const hca_bf16* g, const int32_t* ctx_len, int S,
+                              int H, float scale, const hca_bf16* vha_down,
+                              const hca_bf16* vha_up, int vha_rank,
+                              const hca_paged_cache_t* cache, hca_bf16* out, void* ws,
+                              size_t ws_bytes, hca_stream_t stream);
+
+/*
+ * hca_paged_decode_step — one serving step: hca_paged_append of one token per
+ *   sequence, then hca_paged_decode, in stream order (two launches).
+ */
+hca_status_t hca_paged_decode_step(const hca_bf16* q, const hca_bf16* g, const hca_bf16* k_new,
+                                   const hca_bf16* v_new, const hca_bf16* s_new,
+                                   const int32_t* ctx_len, int S, int H, float scale,
+                                   const hca_bf16* vha_down, const hca_bf16* vha_up, int vha_rank,
+                                   const hca_paged_cache_t* cache, hca_bf16* out, void* ws,
+                                   size_t ws_bytes, hca_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Pages
+ *
+ * Who owns the pages of a pool: page_table [rows, max_pages] int32 (row r:
+ * the pages of a sequence in order, -1 behind them), n_pages [rows] and
+ * ref [num_pages] (rows that name a page; 0 = free), all on the device.
+ * Free pages are handed out lowest number first, in the order of the rows or
+ * pairs, so results do not depend on timing.  ws: at least
+ * hca_pages_workspace_size(rows, num_pages, n) bytes (n: list length, 0 where
+ * there is none), 16-byte aligned, no initialisation; calls that overlap
+ * need one each.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t* page_table;
+  long long table_stride; /* >= max_pages                                      */
+  int rows, max_pages;
+  int32_t* n_pages;
+  int32_t* ref;
+  int num_pages;
+  int page_size; /* entries: 16, 32, 64 or 128                                 */
+} hca_page_table_t;
+
+/* An array of items (pages, or rows of a ring): item x at data + x * item_bytes. */
+typedef struct {
+  void* data;           /* 16-byte aligned                                     */
+  long long item_bytes; /* a multiple of 16                                    */
+} hca_page_array_t;
+
+size_t hca_pages_workspace_size(int rows, int num_pages, int n);
+
+/*
+ * hca_pages_resize — give every row the pages of entries[r] entries
+ *   (ceil(entries[r] / page_size); 0 frees the row, a negative number leaves
+ *   it as it is).  Rows that shrink give up their last pages first (ref - 1);
+ *   rows that grow then take free pages, row by row, while there are any:
+ *   n_pages[r] afterwards tells what row r has.
+ * Layout:  entries [rows] int32 on the device.
+ * Errors:  HCA_ERR_INVALID_ARG / HCA_ERR_UNSUPPORTED on the host as above; on
+ *          the device a row that would exceed max_pages is cut there, and
+ *          inconsistent counts or page numbers are skipped, and reported.
+ */
+hca_status_t hca_pages_resize(const hca_page_table_t* table, const int32_t* entries, void* ws,
+                              size_t ws_bytes, hca_stream_t stream);
+
+/*
+ * hca_pages_fork — branch sequences: the empty row children[i] becomes a copy
+ *   of parents[i] cut at entries[i] entries.  Pages that are full are shared
+ *   (ref + 1); the partly filled one is copied to a fresh page in each of the
+ *   `pools` (arrays of num_pages items), and row parents[i] of each of the
+ *   `rings` (arrays of `rows` items) to row children[i].
+ *   ok[i] = 1 when the branch was made, 0 when no page was free for it.
+ * Layout:  parents, children, entries, ok [n] int32 on the device; pools and
+ *          rings are host arrays of at most 8 arrays together.
+ * Errors:  host checks as above; n > 8192 or more arrays -> HCA_ERR_UNSUPPORTED.
+ *          On the device a pair with a row out of range, a child that has
+ *          pages, is a parent of this call or was named before, or a parent
+ *          with fewer pages than the entries need, is left out (ok[i] = 0) and
+ *          reported.
+ */
+hca_status_t hca_pages_fork(const hca_page_table_t* table, const int32_t* parents,
+                            const int32_t* children, const int32_t* entries, int n,
+                            const hca_page_array_t* pools, int n_pools,
+                            const hca_page_array_t* rings, int n_rings, int32_t* ok, void* ws,
+                            size_t ws_bytes, hca_stream_t stream);
+
+/*
+ * hca_pages_compact — close up a pool: with `live` pages in use, those
+ *   numbered live and above move, in order, into the free ones below; the
+ *   table and ref follow.  live (int32 on the device) receives the count:
+ *   every page from there on is free.
+ * Errors:  as above (at most 8 pools).
+ */
+hca_status_t hca_pages_compact(const hca_page_table_t* table, const hca_page_array_t* pools,
+                               int n_pools, int32_t* live, void* ws, size_t ws_bytes,
+                               hca_stream_t stream);
+
+/*
+ * hca_pages_copy — copy item src[i] to item dst[i] of every array, i < n
+ *   (src, dst int32 on the device; items: number of items of the arrays).
+ *   A source may be named often.  Left out and reported: items out of range,
+ *   and every pair whose destination is named twice or is also a source.
+ *   ws for hca_pages_workspace_size(1, items, n).
+ */
+hca_status_t hca_pages_copy(const hca_page_array_t* arrays, int n_arrays, int items,
+                            const int32_t* src, const int32_t* dst, int n, void* ws,
+                            size_t ws_bytes, hca_stream_t stream);
+
 /*
  * hca_get_device_error — synchronises `stream`, then reads and clears the
  * device-side error word of the current device.  Returns HCA_OK,
