@@ -91,6 +91,8 @@ def lib() -> ctypes.CDLL:
         L.hca_paged_prefill.argtypes = [vp] * 7 + [i, i, i, f, vp, vp, i, pc, vp, vp, sz, vp]
         L.hca_paged_decode.argtypes = [vp, vp, vp, i, i, f, vp, vp, i, pc, vp, vp, sz, vp]
         L.hca_paged_decode_step.argtypes = [vp] * 6 + [i, i, f, vp, vp, i, pc, vp, vp, sz, vp]
+        L.hca_paged_decode_workspace_size.argtypes = [i]
+        L.hca_paged_decode_workspace_size.restype = sz
         L.hca_pages_workspace_size.argtypes = [i, i, i]
         L.hca_pages_workspace_size.restype = sz
         L.hca_pages_resize.argtypes = [pt, vp, vp, sz, vp]
@@ -437,77 +439,113 @@ def decode_e4m3(q: torch.Tensor, ck: torch.Tensor, ck_scale: torch.Tensor, cv: t
 # Paged cache
 # ---------------------------------------------------------------------------
 PAGE_SIZES = (16, 32, 64, 128)
+_SCALE = 1.0 / math.sqrt(HEAD_DIM)
 
 
-def _on(device: torch.device):
-    """The library launches on the current device: make it that of the tensors."""
-    return torch.cuda.device(device)
+def _need(t: torch.Tensor, name: str, shape, dtype, device):
+    """_check, and that t lies on `device`, at the cost of a few attribute reads: a
+    serving step checks a dozen tensors while the GPU waits for its launch."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == device and t.is_contiguous()):
+        _check(t, name, shape, dtype=dtype)
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _check_on(device: torch.device, *tensors):
-    for t, n in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"{n} is on {t.device}, expected {device}")
+def _device_of(t: torch.Tensor, name: str) -> torch.device:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    return t.device
 
 
-def _check_table(page_table: torch.Tensor, rows: int):
+def _call(device: torch.device, name: str, *args):
+    """A library call on the current stream of `device`, made the current device for it."""
+    if torch.cuda.current_device() == device.index:
+        code = getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    else:
+        with torch.cuda.device(device):
+            code = getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if code != 0:
+        raise HCAError(name, code)
+
+
+def _sized(device: torch.device, name: str, *args) -> int:
+    """A workspace size, which depends on the device."""
+    if torch.cuda.current_device() == device.index:
+        return int(getattr(lib(), name)(*args))
+    with torch.cuda.device(device):
+        return int(getattr(lib(), name)(*args))
+
+
+def _cuda(device) -> torch.device:
+    device = torch.device(device)
+    return torch.device("cuda", torch.cuda.current_device()) if device.index is None else device
+
+
+def _workspace(workspace: torch.Tensor, device):
+    _need(workspace, "workspace", (workspace.numel(),), torch.uint8, device)
+    return workspace.data_ptr(), workspace.numel()
+
+
+def _check_table(page_table: torch.Tensor, rows: int, device):
     """A page table: int32 [rows, max_pages] whose rows may lie apart (a view)."""
-    if not isinstance(page_table, torch.Tensor) or page_table.device.type != "cuda":
-        raise ValueError("page_table must be a tensor on a CUDA device")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != rows:
-        raise ValueError(f"page_table must be int32 [{rows}, max_pages], got "
-                         f"{page_table.dtype} {tuple(page_table.shape)}")
+    if (not isinstance(page_table, torch.Tensor) or page_table.dtype is not torch.int32
+            or page_table.dim() != 2 or page_table.shape[0] != rows):
+        raise ValueError(f"page_table must be an int32 tensor [{rows}, max_pages]")
+    if page_table.device != device:
+        raise ValueError(f"page_table is on {page_table.device}, expected {device}")
     cols = page_table.shape[1]
-    if (cols > 1 and page_table.stride(1) != 1) or (rows > 1 and page_table.stride(0) < cols):
+    stride = page_table.stride(0) if rows > 1 else cols
+    if (cols > 1 and page_table.stride(1) != 1) or stride < cols:
         raise ValueError("page_table's rows must be contiguous and not overlap")
-    return cols, (page_table.stride(0) if rows > 1 else cols)
+    return cols, stride
 
 
-def _paged_cache(S, wk, wv, ws, ck_pages, cv_pages, page_table) -> _PagedCache:
-    _check(wk, "wk", (S, WINDOW, HEAD_DIM))
-    _check(wv, "wv", (S, WINDOW, HEAD_DIM))
+def _paged_cache(S, wk, wv, ws, ck_pages, cv_pages, page_table, device) -> _PagedCache:
+    bf16 = torch.bfloat16
+    _need(wk, "wk", (S, WINDOW, HEAD_DIM), bf16, device)
+    _need(wv, "wv", (S, WINDOW, HEAD_DIM), bf16, device)
     if ws is not None:
-        _check(ws, "ws", (S, WINDOW))
+        _need(ws, "ws", (S, WINDOW), bf16, device)
     if not isinstance(ck_pages, torch.Tensor) or ck_pages.dim() != 3:
         raise ValueError("ck_pages must be [num_pages, page_size, 512]")
-    num, size = ck_pages.shape[0], ck_pages.shape[1]
+    num, size, _ = ck_pages.shape
     if size not in PAGE_SIZES:
         raise ValueError(f"pages must hold 16, 32, 64 or 128 entries, got {size}")
-    _check(ck_pages, "ck_pages", (num, size, HEAD_DIM))
-    _check(cv_pages, "cv_pages", (num, size, HEAD_DIM))
-    cols, stride = _check_table(page_table, S)
-    _check_on(wk.device, (wv, "wv"), (ws, "ws"), (ck_pages, "ck_pages"), (cv_pages, "cv_pages"),
-              (page_table, "page_table"))
-    return _PagedCache(wk.data_ptr(), wv.data_ptr(), _ptr(ws), ck_pages.data_ptr() if num else None,
-                       cv_pages.data_ptr() if num else None,
+    _need(ck_pages, "ck_pages", (num, size, HEAD_DIM), bf16, device)
+    _need(cv_pages, "cv_pages", (num, size, HEAD_DIM), bf16, device)
+    cols, stride = _check_table(page_table, S, device)
+    return _PagedCache(wk.data_ptr(), wv.data_ptr(), None if ws is None else ws.data_ptr(),
+                       ck_pages.data_ptr() if num else None, cv_pages.data_ptr() if num else None,
                        page_table.data_ptr() if cols else None, stride, cols, num, size)
 
 
 def _check_chunk(k_new, v_new, s_new, q_start, ctx_len, device):
     S = ctx_len.shape[0]
     N = k_new.shape[0]
-    _check(ctx_len, "ctx_len", (S,), dtype=torch.int32)
-    _check(k_new, "k_new", (N, HEAD_DIM))
-    _check(v_new, "v_new", (N, HEAD_DIM))
-    _check(s_new, "s_new", (N,))
+    bf16 = torch.bfloat16
+    _need(ctx_len, "ctx_len", (S,), torch.int32, device)
+    _need(k_new, "k_new", (N, HEAD_DIM), bf16, device)
+    _need(v_new, "v_new", (N, HEAD_DIM), bf16, device)
+    _need(s_new, "s_new", (N,), bf16, device)
     if q_start is not None:
-        _check(q_start, "q_start", (S + 1,), dtype=torch.int32)
+        _need(q_start, "q_start", (S + 1,), torch.int32, device)
     elif N != S:
         raise ValueError(f"{N} new tokens for {S} sequences need q_start")
-    _check_on(device, (ctx_len, "ctx_len"), (k_new, "k_new"), (v_new, "v_new"), (s_new, "s_new"),
-              (q_start, "q_start"))
     return S, N
 
 
 def _attend_args(q, g, out, vha, rows, scale, device):
-    _check(q, "q", (rows, HEADS, HEAD_DIM))
-    _check(g, "g", (rows, HEADS, HEAD_DIM))
+    shape = (rows, HEADS, HEAD_DIM)
+    _need(q, "q", shape, torch.bfloat16, device)
+    _need(g, "g", shape, torch.bfloat16, device)
     if out is None:
         out = torch.empty_like(q)
-    _check(out, "out", (rows, HEADS, HEAD_DIM))
-    _check_on(device, (q, "q"), (g, "g"), (out, "out"))
+    else:
+        _need(out, "out", shape, torch.bfloat16, device)
     down, up, r = (None, None, 0) if vha is None else _check_vha(vha, device)
-    return (out, 1.0 / math.sqrt(HEAD_DIM) if scale is None else scale, _ptr(down), _ptr(up), r)
+    return out, _SCALE if scale is None else scale, _ptr(down), _ptr(up), r
 
 
 def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, s_new: torch.Tensor,
@@ -522,23 +560,20 @@ def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, s_new: torch.Tensor,
     [S, 128, 512] and ws [S, 128] rings; ck_pages, cv_pages
     [num_pages, page_size, 512]; page_table [S, max_pages] int32: entry j of
     sequence i is row j % page_size of page page_table[i, j // page_size]."""
-    device = wk.device
+    device = _device_of(wk, "wk")
     S, N = _check_chunk(k_new, v_new, s_new, q_start, ctx_len, device)
-    cache = _paged_cache(S, wk, wv, ws, ck_pages, cv_pages, page_table)
+    cache = _paged_cache(S, wk, wv, ws, ck_pages, cv_pages, page_table, device)
     if N == 0:
         return
-    with _on(device):
-        _ok("hca_paged_append", lib().hca_paged_append(
-            k_new.data_ptr(), v_new.data_ptr(), s_new.data_ptr(), _ptr(q_start),
-            ctx_len.data_ptr(), S, N, ctypes.byref(cache), _stream(device)))
+    _call(device, "hca_paged_append", k_new.data_ptr(), v_new.data_ptr(), s_new.data_ptr(),
+          _ptr(q_start), ctx_len.data_ptr(), S, N, ctypes.byref(cache))
 
 
 def paged_prefill_workspace(S: int, N: int, device) -> torch.Tensor:
     """Scratch for paged_prefill of N new tokens of S sequences (reusable across calls)."""
-    device = torch.device(device)
-    with _on(device):
-        return torch.empty((int(lib().hca_paged_prefill_workspace_size(S, N)),),
-                           dtype=torch.uint8, device=device)
+    device = _cuda(device)
+    return torch.empty((_sized(device, "hca_paged_prefill_workspace_size", S, N),),
+                       dtype=torch.uint8, device=device)
 
 
 def paged_prefill(q: torch.Tensor, g: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -552,32 +587,27 @@ def paged_prefill(q: torch.Tensor, g: torch.Tensor, k_new: torch.Tensor, v_new: 
     q, g [N, 64, 512], packed like k_new -> out [N, 64, 512] bf16 (rows from
     q_start[S] on are not written).  The other arguments are paged_append's;
     `workspace` comes from paged_prefill_workspace; `vha` as for decode."""
-    device = wk.device
+    device = _device_of(wk, "wk")
     if q_start is None:
         raise ValueError("paged_prefill needs q_start (paged_decode_step takes one token each)")
     S, N = _check_chunk(k_new, v_new, s_new, q_start, ctx_len, device)
-    cache = _paged_cache(S, wk, wv, ws, ck_pages, cv_pages, page_table)
+    cache = _paged_cache(S, wk, wv, ws, ck_pages, cv_pages, page_table, device)
     out, scale, down, up, r = _attend_args(q, g, out, vha, N, scale, device)
     if N == 0:
         return out
     if workspace is None:
         workspace = paged_prefill_workspace(S, N, device)
-    _check(workspace, "workspace", dtype=torch.uint8)
-    _check_on(device, (workspace, "workspace"))
-    with _on(device):
-        _ok("hca_paged_prefill", lib().hca_paged_prefill(
-            q.data_ptr(), g.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), s_new.data_ptr(),
-            q_start.data_ptr(), ctx_len.data_ptr(), S, N, HEADS, ctypes.c_float(scale), down, up, r,
-            ctypes.byref(cache), out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-            _stream(device)))
+    _call(device, "hca_paged_prefill", q.data_ptr(), g.data_ptr(), k_new.data_ptr(),
+          v_new.data_ptr(), s_new.data_ptr(), q_start.data_ptr(), ctx_len.data_ptr(), S, N, HEADS,
+          scale, down, up, r, ctypes.byref(cache), out.data_ptr(), *_workspace(workspace, device))
     return out
 
 
 def paged_decode_workspace(S: int, device) -> torch.Tensor:
     """A zero-filled workspace for paged_decode of up to S sequences (reusable across calls)."""
-    device = torch.device(device)
-    with _on(device):
-        return decode_workspace(S, device)
+    device = _cuda(device)
+    return torch.zeros((_sized(device, "hca_paged_decode_workspace_size", S),),
+                       dtype=torch.uint8, device=device)
 
 
 def paged_decode(q: torch.Tensor, ck_pages: torch.Tensor, cv_pages: torch.Tensor,
@@ -588,21 +618,15 @@ def paged_decode(q: torch.Tensor, ck_pages: torch.Tensor, cv_pages: torch.Tensor
     """decode over a paged cache: one query per sequence, q, g [S, 64, 512];
     the cache (see paged_append) already holds its token.  A workspace passed
     in comes from paged_decode_workspace."""
-    device = wk.device
+    device = _device_of(wk, "wk")
     S = ctx_len.shape[0]
-    _check(ctx_len, "ctx_len", (S,), dtype=torch.int32)
-    _check_on(device, (ctx_len, "ctx_len"))
-    cache = _paged_cache(S, wk, wv, None, ck_pages, cv_pages, page_table)
+    _need(ctx_len, "ctx_len", (S,), torch.int32, device)
+    cache = _paged_cache(S, wk, wv, None, ck_pages, cv_pages, page_table, device)
     out, scale, down, up, r = _attend_args(q, g, out, vha, S, scale, device)
     if workspace is None:
         workspace = paged_decode_workspace(S, device)
-    _check(workspace, "workspace", dtype=torch.uint8)
-    _check_on(device, (workspace, "workspace"))
-    with _on(device):
-        _ok("hca_paged_decode", lib().hca_paged_decode(
-            q.data_ptr(), g.data_ptr(), ctx_len.data_ptr(), S, HEADS, ctypes.c_float(scale), down,
-            up, r, ctypes.byref(cache), out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-            _stream(device)))
+    _call(device, "hca_paged_decode", q.data_ptr(), g.data_ptr(), ctx_len.data_ptr(), S, HEADS,
+          scale, down, up, r, ctypes.byref(cache), out.data_ptr(), *_workspace(workspace, device))
     return out
 
 
@@ -614,32 +638,27 @@ def paged_decode_step(q: torch.Tensor, g: torch.Tensor, k_new: torch.Tensor, v_n
                       out: Optional[torch.Tensor] = None, vha=None) -> torch.Tensor:
     """One serving step: paged_append of one token per sequence (k_new, v_new
     [S, 512]; s_new [S]), then paged_decode of their queries q, g [S, 64, 512]."""
-    device = wk.device
+    device = _device_of(wk, "wk")
     S, _ = _check_chunk(k_new, v_new, s_new, None, ctx_len, device)
-    cache = _paged_cache(S, wk, wv, ws, ck_pages, cv_pages, page_table)
+    cache = _paged_cache(S, wk, wv, ws, ck_pages, cv_pages, page_table, device)
     out, scale, down, up, r = _attend_args(q, g, out, vha, S, scale, device)
     if workspace is None:
         workspace = paged_decode_workspace(S, device)
-    _check(workspace, "workspace", dtype=torch.uint8)
-    _check_on(device, (workspace, "workspace"))
-    with _on(device):
-        _ok("hca_paged_decode_step", lib().hca_paged_decode_step(
-            q.data_ptr(), g.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), s_new.data_ptr(),
-            ctx_len.data_ptr(), S, HEADS, ctypes.c_float(scale), down, up, r, ctypes.byref(cache),
-            out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(device)))
+    _call(device, "hca_paged_decode_step", q.data_ptr(), g.data_ptr(), k_new.data_ptr(),
+          v_new.data_ptr(), s_new.data_ptr(), ctx_len.data_ptr(), S, HEADS, scale, down, up, r,
+          ctypes.byref(cache), out.data_ptr(), *_workspace(workspace, device))
     return out
 
 
-def _page_table(page_table, n_pages, ref, page_size: int) -> _PageTable:
+def _page_table(page_table, n_pages, ref, page_size: int, device) -> _PageTable:
     if page_size not in PAGE_SIZES:
         raise ValueError(f"pages must hold 16, 32, 64 or 128 entries, got {page_size}")
-    rows = n_pages.shape[0]
-    _check(n_pages, "n_pages", (rows,), dtype=torch.int32)
-    _check(ref, "ref", (ref.numel(),), dtype=torch.int32)
-    cols, stride = _check_table(page_table, rows)
-    _check_on(page_table.device, (n_pages, "n_pages"), (ref, "ref"))
+    rows, num = n_pages.shape[0], ref.shape[0]
+    _need(n_pages, "n_pages", (rows,), torch.int32, device)
+    _need(ref, "ref", (num,), torch.int32, device)
+    cols, stride = _check_table(page_table, rows, device)
     return _PageTable(page_table.data_ptr(), stride, rows, cols, n_pages.data_ptr(),
-                      ref.data_ptr(), ref.numel(), page_size)
+                      ref.data_ptr(), num, page_size)
 
 
 def _page_arrays(arrays, items: int, what: str, device):
@@ -650,19 +669,17 @@ def _page_arrays(arrays, items: int, what: str, device):
             raise ValueError(f"{what}[{i}] must be a tensor on {device}")
         if not t.is_contiguous() or t.dim() < 2 or t.shape[0] != items:
             raise ValueError(f"{what}[{i}] must be contiguous [{items}, ...], got {tuple(t.shape)}")
-        nbytes = t.numel() // items * t.element_size()
+        nbytes = t.nbytes // items
         if nbytes < 16 or nbytes % 16:
             raise ValueError(f"{what}[{i}]: items of {nbytes} bytes, a multiple of 16 is needed")
-        out[i] = _PageArray(t.data_ptr(), nbytes)
+        out[i].data, out[i].item_bytes = t.data_ptr(), nbytes
     return out
 
 
 def _pages_workspace(workspace, rows, num_pages, n, device):
-    size = int(lib().hca_pages_workspace_size(rows, num_pages, n))
     if workspace is None:
-        return torch.empty((size,), dtype=torch.uint8, device=device)
-    _check(workspace, "workspace", dtype=torch.uint8)
-    _check_on(device, (workspace, "workspace"))
+        workspace = torch.empty((_sized(device, "hca_pages_workspace_size", rows, num_pages, n),),
+                                dtype=torch.uint8, device=device)
     return workspace
 
 
@@ -675,15 +692,12 @@ def resize_pages(page_table: torch.Tensor, n_pages: torch.Tensor, ref: torch.Ten
     int32 on the device.  0 frees a row, a negative number leaves it.  Rows
     shrink first; rows that grow take the lowest free pages, row by row, while
     there are any (n_pages[r] tells what row r has)."""
-    device = page_table.device
-    table = _page_table(page_table, n_pages, ref, page_size)
-    _check(entries, "entries", (table.rows,), dtype=torch.int32)
-    _check_on(device, (entries, "entries"))
-    with _on(device):
-        workspace = _pages_workspace(workspace, table.rows, table.num_pages, 0, device)
-        _ok("hca_pages_resize", lib().hca_pages_resize(
-            ctypes.byref(table), entries.data_ptr(), workspace.data_ptr(), workspace.numel(),
-            _stream(device)))
+    device = _device_of(page_table, "page_table")
+    table = _page_table(page_table, n_pages, ref, page_size, device)
+    _need(entries, "entries", (table.rows,), torch.int32, device)
+    workspace = _pages_workspace(workspace, table.rows, table.num_pages, 0, device)
+    _call(device, "hca_pages_resize", ctypes.byref(table), entries.data_ptr(),
+          *_workspace(workspace, device))
 
 
 def fork_pages(page_table: torch.Tensor, n_pages: torch.Tensor, ref: torch.Tensor,
@@ -696,23 +710,20 @@ def fork_pages(page_table: torch.Tensor, n_pages: torch.Tensor, ref: torch.Tenso
     ([num_pages, ...] tensors), and row parents[i] of every ring ([R, ...]) to
     row children[i].  Returns ok [n] int32: 0 where no page was free (or the
     pair was refused, which device_error() reports)."""
-    device = page_table.device
-    table = _page_table(page_table, n_pages, ref, page_size)
+    device = _device_of(page_table, "page_table")
+    table = _page_table(page_table, n_pages, ref, page_size, device)
     n = parents.shape[0]
     for t, name in ((parents, "parents"), (children, "children"), (entries, "entries")):
-        _check(t, name, (n,), dtype=torch.int32)
-        _check_on(device, (t, name))
+        _need(t, name, (n,), torch.int32, device)
     pool_arrays = _page_arrays(pools, table.num_pages, "pools", device)
     ring_arrays = _page_arrays(rings, table.rows, "rings", device)
     ok = torch.empty((n,), dtype=torch.int32, device=device)
     if n == 0:
         return ok
-    with _on(device):
-        workspace = _pages_workspace(workspace, table.rows, table.num_pages, n, device)
-        _ok("hca_pages_fork", lib().hca_pages_fork(
-            ctypes.byref(table), parents.data_ptr(), children.data_ptr(), entries.data_ptr(), n,
-            pool_arrays, len(pools), ring_arrays, len(rings), ok.data_ptr(), workspace.data_ptr(),
-            workspace.numel(), _stream(device)))
+    workspace = _pages_workspace(workspace, table.rows, table.num_pages, n, device)
+    _call(device, "hca_pages_fork", ctypes.byref(table), parents.data_ptr(), children.data_ptr(),
+          entries.data_ptr(), n, pool_arrays, len(pools), ring_arrays, len(rings), ok.data_ptr(),
+          *_workspace(workspace, device))
     return ok
 
 
@@ -721,15 +732,13 @@ def compact_pages(page_table: torch.Tensor, n_pages: torch.Tensor, ref: torch.Te
     """Close up a pool: the pages in use take the lowest numbers, page_table,
     ref and the contents of every pool ([num_pages, ...]) follow.  Returns the
     number of pages in use ([1] int32 on the device); all others are free."""
-    device = page_table.device
-    table = _page_table(page_table, n_pages, ref, PAGE_SIZES[0])
+    device = _device_of(page_table, "page_table")
+    table = _page_table(page_table, n_pages, ref, PAGE_SIZES[0], device)
     arrays = _page_arrays(pools, table.num_pages, "pools", device)
     live = torch.empty((1,), dtype=torch.int32, device=device)
-    with _on(device):
-        workspace = _pages_workspace(workspace, table.rows, table.num_pages, 0, device)
-        _ok("hca_pages_compact", lib().hca_pages_compact(
-            ctypes.byref(table), arrays, len(pools), live.data_ptr(), workspace.data_ptr(),
-            workspace.numel(), _stream(device)))
+    workspace = _pages_workspace(workspace, table.rows, table.num_pages, 0, device)
+    _call(device, "hca_pages_compact", ctypes.byref(table), arrays, len(pools), live.data_ptr(),
+          *_workspace(workspace, device))
     return live
 
 
@@ -741,18 +750,16 @@ def copy_pages(arrays, src: torch.Tensor, dst: torch.Tensor,
     by device_error()."""
     if len(arrays) == 0:
         return
-    n, items, device = src.shape[0], arrays[0].shape[0], arrays[0].device
-    for t, name in ((src, "src"), (dst, "dst")):
-        _check(t, name, (n,), dtype=torch.int32)
-        _check_on(device, (t, name))
+    device = _device_of(arrays[0], "arrays[0]")
+    n, items = src.shape[0], arrays[0].shape[0]
+    _need(src, "src", (n,), torch.int32, device)
+    _need(dst, "dst", (n,), torch.int32, device)
     item_arrays = _page_arrays(arrays, items, "arrays", device)
     if n == 0:
         return
-    with _on(device):
-        workspace = _pages_workspace(workspace, 1, items, n, device)
-        _ok("hca_pages_copy", lib().hca_pages_copy(
-            item_arrays, len(arrays), items, src.data_ptr(), dst.data_ptr(), n,
-            workspace.data_ptr(), workspace.numel(), _stream(device)))
+    workspace = _pages_workspace(workspace, 1, items, n, device)
+    _call(device, "hca_pages_copy", item_arrays, len(arrays), items, src.data_ptr(),
+          dst.data_ptr(), n, *_workspace(workspace, device))
 
 
 def device_error(device: Optional[torch.device] = None) -> Tuple[int, int]:

@@ -112,11 +112,16 @@ constexpr uint32_t kTmemO = 0, kTmemS0 = 256, kTmemS1 = 320, kTmemCols = 512;
 // l and stored with value column 128c + r at [r][c] (one 8-byte store per head
 // and TMEM lane); then [slots][2][64] fp32 (m, l)
 // in log2 units.  slots = grid + S.
-__host__ __device__ inline size_t ws_o_bytes(int slots) {
-  return static_cast<size_t>(slots) * kHeads * kDim * 2;
+// Paged cache: [slots][64 heads][512] fp32 partial O, columns in order.  In
+// bf16 the partials' rounding adds in squares to that of the probabilities and
+// of the output (each 2^-8 at most): 2.8e-3 off the 64-bit result, 2.3e-3 with
+// fp32 partials (relative 2-norm, 64 x 131072 tokens), for 66 KB more per slot
+// through L2.
+__host__ __device__ inline size_t ws_o_bytes(int slots, bool f32 = false) {
+  return static_cast<size_t>(slots) * kHeads * kDim * (f32 ? 4 : 2);
 }
-__host__ __device__ inline size_t ws_bytes(int slots) {
-  return ws_o_bytes(slots) + static_cast<size_t>(slots) * 2 * kHeads * 4;
+__host__ __device__ inline size_t ws_bytes(int slots, bool f32 = false) {
+  return ws_o_bytes(slots, f32) + static_cast<size_t>(slots) * 2 * kHeads * 4;
 }
 
 struct Params {
@@ -124,7 +129,7 @@ struct Params {
   int S;
   int max_nc;
   float scale_log2;
-  uint16_t* ws_o;      // [slots][64][128][4] bf16
+  uint16_t* ws_o;      // [slots][64][128][4] bf16 (paged cache: [slots][64][512] fp32)
   float* ws_ml;        // [slots][2][64]
   long long* seq_tile; // [S + 1] exclusive prefix of tile counts (plan kernel, S > kInlineSeqs)
   unsigned long long* gsync;  // grid barrier arrivals (zero before first use, see below)
@@ -147,6 +152,7 @@ struct Params {
   const int* row_of;   // [S] table row of each query, null: query s has row s
   const int* win_row;  // [S] first window row of each query, null: a ring at 128 s
   const int* count;    // number of queries on the device (at most S), null: S
+  int plan_early;      // ctx_len is older than the kernel in front: plan before waiting for it
 };
 
 __device__ __forceinline__ int nc_of_len(int L) { return L >= 128 ? (L - 128) / 128 : 0; }
@@ -384,7 +390,7 @@ struct CombSeq {
 // holds data (an empty split's run was never copied), `seq_a(f)` whether run
 // f belongs to the group's first sequence.  A row of the other sequence reads
 // some in-bounds words and replaces them by zeros with weight 0.
-template <int NK, int NU, typename RunOf, typename SeqA>
+template <bool kF32, int NK, int NU, typename RunOf, typename SeqA>
 __device__ __forceinline__ void merge_runs(const uint8_t* smem, int fs, int fe,
                                            const bool (&rowA)[4], const int (&hrow)[4],
                                            const uint32_t (&roff)[4], const float (&Mu)[4],
@@ -392,7 +398,8 @@ __device__ __forceinline__ void merge_runs(const uint8_t* smem, int fs, int fe,
                                            SeqA&& seq_a) {
 #pragma unroll 1
   for (int f = fs; f < fe; f += NU) {
-    uint4 x[NU][NK][2];
+    constexpr int NX = kF32 ? 4 : 2;
+    uint4 x[NU][NK][NX];
     float w[NU][NK];
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
@@ -405,25 +412,36 @@ __device__ __forceinline__ void merge_runs(const uint8_t* smem, int fs, int fe,
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
         const uint4* row = reinterpret_cast<const uint4*>(smem + kSmemQ + base + roff[k]);
-        x[u][k][0] = row[0];
-        x[u][k][1] = row[1];
+#pragma unroll
+        for (int q = 0; q < NX; ++q) x[u][k][q] = row[kF32 ? 32 * q : q];
         const float mi = ml[hrow[k]], li = ml[64 + hrow[k]];
         // the partial row is normalised: its weight carries its sum l
         const bool mine = live && rowA[k] == inA;
         w[u][k] = (mine && mi != -INFINITY) ? li * ex2_approx(mi - Mu[k]) : 0.f;
         if (!mine) {  // not this row's data (or never copied): may hold anything
-          x[u][k][0] = make_uint4(0u, 0u, 0u, 0u);
-          x[u][k][1] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int q = 0; q < NX; ++q) x[u][k][q] = make_uint4(0u, 0u, 0u, 0u);
         }
       }
     }
     // lane l: rows 4l + t (t = 0..3) of the [128][4] layout, i.e. value
-    // columns 128c + 4l + t, in words (t, c = 0|1) and (t, c = 2|3)
+    // columns 128c + 4l + t, in words (t, c = 0|1) and (t, c = 2|3); fp32: the
+    // same columns, four in a row for each c
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
         L[k] += w[u][k];
+        if constexpr (kF32) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            acc[k][4 * q] = fmaf(w[u][k], __uint_as_float(x[u][k][q].x), acc[k][4 * q]);
+            acc[k][4 * q + 1] = fmaf(w[u][k], __uint_as_float(x[u][k][q].y), acc[k][4 * q + 1]);
+            acc[k][4 * q + 2] = fmaf(w[u][k], __uint_as_float(x[u][k][q].z), acc[k][4 * q + 2]);
+            acc[k][4 * q + 3] = fmaf(w[u][k], __uint_as_float(x[u][k][q].w), acc[k][4 * q + 3]);
+          }
+          continue;
+        }
         const uint32_t wd[8] = {x[u][k][0].x, x[u][k][0].y, x[u][k][0].z, x[u][k][0].w,
                                 x[u][k][1].x, x[u][k][1].y, x[u][k][1].z, x[u][k][1].w};
 #pragma unroll
@@ -438,20 +456,24 @@ __device__ __forceinline__ void merge_runs(const uint8_t* smem, int fs, int fe,
   }
 }
 
-template <typename GridArrive, typename GridWait>
+// `split`: CTAs the tiles are split over (paged cache: no more than there are
+// tiles, so that no split is empty; `grid` of them merge rows either way).
+template <bool kF32, typename GridArrive, typename GridWait>
 __device__ __forceinline__ void combine_cta(const Params& p, const long long* tiles, int grid,
+                                            int split,
                                             uint8_t* smem, uint32_t sbase, uint32_t bar_comb,
                                             volatile int* abort_flag, int warp, int lane,
                                             GridArrive&& grid_arrive, GridWait&& grid_wait) {
   const long long N = tiles[p.S];
   // CTA that owns global tile x: ceil((x + 1) * grid / N) - 1
   auto owner = [&](long long x) -> int {
-    return static_cast<int>(div_nn((x + 1) * grid + N - 1, N)) - 1;
+    return static_cast<int>(div_nn((x + 1) * split + N - 1, N)) - 1;
   };
   // With at least one tile per CTA every split is non-empty: the 64-bit
   // divisions of the general test are kept off the common path.
-  const bool dense = N >= grid;
-  auto nonempty = [&](int c) { return dense || div_nn(N * c, grid) < div_nn(N * (c + 1), grid); };
+  constexpr uint32_t kRow = kDim * (kF32 ? 4 : 2);   // bytes of a partial row
+  const bool dense = kF32 || N >= split;
+  auto nonempty = [&](int c) { return dense || div_nn(N * c, split) < div_nn(N * (c + 1), split); };
   auto seq = [&](int s, int h0, int nh) -> CombSeq {
     CombSeq q;
     q.s = s;
@@ -475,8 +497,8 @@ __device__ __forceinline__ void combine_cta(const Params& p, const long long* ti
     const CombSeq A = seq(sA, hA, nA);
     const CombSeq B = (ng > nA) ? seq(sA + 1, 0, ng - nA) : CombSeq{sA + 1, 0, 0, 0, 0};
     const int nItems = A.n + B.n;
-    const uint32_t szA = static_cast<uint32_t>(A.nh) * kDim * 2;
-    const uint32_t szB = static_cast<uint32_t>(B.nh) * kDim * 2;
+    const uint32_t szA = static_cast<uint32_t>(A.nh) * kRow;
+    const uint32_t szB = static_cast<uint32_t>(B.nh) * kRow;
 
     // this warp's rows: merge state and sigmoid(g)
     float M[4], L[4], acc[4][16];
@@ -538,7 +560,8 @@ __device__ __forceinline__ void combine_cta(const Params& p, const long long* ti
           const uint32_t sz = inA ? szA : szB;
           if (nonempty(c)) {
             const size_t slot = static_cast<size_t>(c + q.s);
-            const uint16_t* src = p.ws_o + (slot * kHeads + q.h0) * kDim;
+            const uint8_t* src = reinterpret_cast<const uint8_t*>(p.ws_o) +
+                                 (slot * kHeads + q.h0) * kRow;
             asm volatile(
                 "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes"
                 " [%0], [%1], %2, [%3];" ::"r"(sbase + kSmemQ + off),
@@ -600,7 +623,7 @@ __device__ __forceinline__ void combine_cta(const Params& p, const long long* ti
         rowA[k] = i < A.nh;
         const int r = rowA[k] ? i : i - A.nh;
         hrow[k] = (rowA[k] ? A.h0 : B.h0) + r;
-        roff[k] = static_cast<uint32_t>(r) * kDim * 2 + 32u * lane;
+        roff[k] = static_cast<uint32_t>(r) * kRow + (kF32 ? 16u : 32u) * lane;
       }
       auto run_of = [&](int f, bool& live) -> uint32_t {
         const bool inA = f < A.n;
@@ -612,13 +635,13 @@ __device__ __forceinline__ void combine_cta(const Params& p, const long long* ti
       auto seq_a = [&](int f) { return f < A.n; };
       const int nk = ng > warp ? min(4, (ng - warp + 6) / 7) : 0;
       if (nk == 4)
-        merge_runs<4, 1>(smem, fs, fe, rowA, hrow, roff, Mu, L, acc, run_of, seq_a);
+        merge_runs<kF32, 4, 1>(smem, fs, fe, rowA, hrow, roff, Mu, L, acc, run_of, seq_a);
       else if (nk == 3)
-        merge_runs<3, 1>(smem, fs, fe, rowA, hrow, roff, Mu, L, acc, run_of, seq_a);
+        merge_runs<kF32, 3, 1>(smem, fs, fe, rowA, hrow, roff, Mu, L, acc, run_of, seq_a);
       else if (nk == 2)
-        merge_runs<2, 2>(smem, fs, fe, rowA, hrow, roff, Mu, L, acc, run_of, seq_a);
+        merge_runs<kF32, 2, 2>(smem, fs, fe, rowA, hrow, roff, Mu, L, acc, run_of, seq_a);
       else if (nk == 1)
-        merge_runs<1, 4>(smem, fs, fe, rowA, hrow, roff, Mu, L, acc, run_of, seq_a);
+        merge_runs<kF32, 1, 4>(smem, fs, fe, rowA, hrow, roff, Mu, L, acc, run_of, seq_a);
       __syncthreads();  // the next batch overwrites the buffers
       fs = fe;
     }
@@ -788,9 +811,6 @@ template <bool kF8, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_kernel(const __grid_constant__ Maps maps, const Params p0) {
   Params p = p0;
-  if constexpr (kPaged) {
-    if (p.count != nullptr) p.S = min(max(*p.count, 0), p0.S);
-  }
   constexpr int NS = kF8 ? kStagesF8 : kStages;   // ring stages
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte aligned, derived from smem_raw itself so that the compiler
@@ -850,8 +870,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool inl = p0.S <= kInlineSeqs;   // as the launch decided
   long long* sT = reinterpret_cast<long long*>(smem + kSmemTiles);
   int* sL = reinterpret_cast<int*>(smem + kSmemCtx);
+  if constexpr (kPaged) {
+    // launched while the append (or the plan) may still run: what follows reads its results
+    if (inl && p.plan_early) inline_plan(p, sT, sL);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (p.count != nullptr) p.S = min(max(*p.count, 0), p0.S);
+  }
   if (inl) {
-    inline_plan(p, sT, sL);
+    if (!kPaged || !p.plan_early) inline_plan(p, sT, sL);
   } else {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __syncthreads();
@@ -861,8 +887,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long* tiles = inl ? sT : p.seq_tile;
   const int* lens = inl ? sL : p.ctx_len;
   const long long N = tiles[p.S];
-  const long long A0 = div_nn(N * blockIdx.x, gridDim.x);
-  const long long A1 = div_nn(N * (blockIdx.x + 1), gridDim.x);
+  // CTAs the tiles are split over: with fewer tiles than CTAs one tile each, so
+  // that merging never looks at splits without a tile (81 us instead of a few
+  // for one short sequence)
+  const int split = kPaged ? static_cast<int>(min(static_cast<long long>(gridDim.x), max(N, 1LL)))
+                           : static_cast<int>(gridDim.x);
+  const bool splits = !kPaged || static_cast<int>(blockIdx.x) < split;
+  const long long A0 = splits ? div_nn(N * blockIdx.x, split) : 0;
+  const long long A1 = splits ? div_nn(N * (blockIdx.x + 1), split) : 0;
   if (A0 < A1) {  // uniform across the CTA; a CTA without tiles only helps combine
 
   // Segments: maximal runs of this CTA's tiles inside one sequence.
@@ -1479,6 +1511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_bar_sync(1, 128);
       const int slot = blockIdx.x + s;
       uint2* wo = reinterpret_cast<uint2*>(p.ws_o + static_cast<size_t>(slot) * kHeads * kDim) + key;
+      float* wf = reinterpret_cast<float*>(p.ws_o) + static_cast<size_t>(slot) * kHeads * kDim + key;
 #pragma unroll 1
       for (int hh = 0; hh < 64; hh += 16) {
         uint32_t o[64];
@@ -1489,6 +1522,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const float inv = red[R_ALPHA + hh + i];
+          if constexpr (kPaged) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              wf[(hh + i) * kDim + 128 * c] = __uint_as_float(o[16 * c + i]) * inv;
+            continue;
+          }
           wo[(hh + i) * kKeyTile] =
               make_uint2(pack_bf16x2(__uint_as_float(o[i]) * inv, __uint_as_float(o[16 + i]) * inv),
                          pack_bf16x2(__uint_as_float(o[32 + i]) * inv,
@@ -1565,8 +1604,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) fence_proxy_async_all();
     __syncthreads();
   };
-  combine_cta(p, tiles, gridDim.x, smem, sbase, bar(B_COMB), abort_flag, warp, lane,
-              grid_arrive, grid_wait);
+  combine_cta<kPaged>(p, tiles, gridDim.x, split, smem, sbase, bar(B_COMB), abort_flag, warp, lane,
+                      grid_arrive, grid_wait);
   if (!kF8 && p.vha_rank > 0) {
     // the combine's buffers are free once every warp is here
     float* fd = reinterpret_cast<float*>(smem + kSmemQ);   // [64][r8]

@@ -7,6 +7,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -150,6 +151,21 @@ int prefill_max_clusters() {
   return n;
 }
 
+// Runs `f` once for every device the process uses (with that device current):
+// kernel attributes are per-device properties.  `kTag` names what is set.
+template <int kTag, typename F>
+cudaError_t once_per_device(F&& f) {
+  static std::atomic<bool> done[kMaxDevices];
+  int dev = 0;
+  const cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= kMaxDevices) return f();
+  if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t set = f();
+  if (set == cudaSuccess) done[dev].store(true, std::memory_order_release);
+  return set;
+}
+
 // The decode pass: for more than kInlineSeqs sequences the plan kernel first
 // (the decode kernel then starts early and waits for it inside), else the
 // decode kernel alone, which plans for itself.  Cooperative either way: the
@@ -158,8 +174,10 @@ template <bool kF8, bool kPaged = false>
 cudaError_t launch_decode(const hca::decode::Maps& maps, const hca::decode::Params& prm, int grid,
                           cudaStream_t stream) {
   namespace D = hca::decode;
-  cudaError_t err = cudaFuncSetAttribute(D::decode_kernel<kF8, kPaged>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, D::kSmemAlloc);
+  cudaError_t err = once_per_device<kF8 ? (kPaged ? 3 : 2) : (kPaged ? 1 : 0)>([] {
+    return cudaFuncSetAttribute(D::decode_kernel<kF8, kPaged>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, D::kSmemAlloc);
+  });
   if (err != cudaSuccess) return err;
   const bool inl = prm.S <= D::kInlineSeqs;
   if (!inl) {
@@ -178,7 +196,7 @@ cudaError_t launch_decode(const hca::decode::Maps& maps, const hca::decode::Para
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = inl ? 1 : 2;
+  cfg.numAttrs = inl && !kPaged ? 1 : 2;
   return cudaLaunchKernelEx(&cfg, D::decode_kernel<kF8, kPaged>, maps, prm);
 }
 
@@ -186,10 +204,15 @@ hca_status_t launch_status() {
   return cudaGetLastError() == cudaSuccess ? HCA_OK : HCA_ERR_CUDA;
 }
 
+// SM count of the current device, asked once for each
 int device_sms() {
+  static std::atomic<int> known[kMaxDevices];
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  if (dev >= 0 && dev < kMaxDevices && (sms = known[dev].load(std::memory_order_relaxed)) > 0)
+    return sms;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
+  if (dev >= 0 && dev < kMaxDevices) known[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
 

@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ float red[2][4];
   __shared__ int cnt[4];
   __shared__ float part[8][kBlk + 4];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5;
   const int u = blockIdx.x;
   const int which = blockIdx.y >> 2, quarter = blockIdx.y & 3;
@@ -219,8 +220,11 @@ constexpr int kFinishThreads = 256;
 // grid (S, kFinishY)
 __global__ void __launch_bounds__(kFinishThreads)
     finish_kernel(const Chunk c, const Cache cache, const Queries qr) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int i = blockIdx.x, tid = threadIdx.x;
   const Span sp = span_of(c, i, blockIdx.y == 0 && tid == 0);
+  // launched while entries_kernel may still read the rings
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (qr.count != nullptr) {
     const int base = raw_base(sp, i);
     for (int r = blockIdx.y * kFinishThreads + tid; r < sp.n; r += kFinishY * kFinishThreads) {
@@ -259,6 +263,7 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const Chunk c, const Cac
   __shared__ float w[kBlk];
   __shared__ float red[2][4];
   __shared__ float part[8][kBlk + 4];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int i = blockIdx.x, tid = threadIdx.x, warp = tid >> 5;
   const int which = blockIdx.y >> 2, quarter = blockIdx.y & 3;
   const int L = c.ctx_len[i];

@@ -58,6 +58,23 @@ hca_status_t chunk_args(hca::paged::Chunk& c, const hca_bf16* k_new, const hca_b
   return HCA_OK;
 }
 
+// A launch that may begin while the kernel before it on the stream still runs
+// (it waits for its results inside).
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream,
+                          const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // grid.x of entries_kernel: the units of all sequences
 long long entry_units(int S, int N) {
   return N / hca::paged::kBlk + static_cast<long long>(hca::paged::kUnitsExtra) * S;
@@ -75,8 +92,8 @@ hca_status_t paged_attend(const hca::paged::Cache& c, const hca_bf16* q, const h
   prm.max_nc = c.max_pages << c.page_shift;
   prm.gsync = reinterpret_cast<unsigned long long*>(ws);
   prm.ws_o = reinterpret_cast<uint16_t*>(ws + 256);
-  prm.ws_ml = reinterpret_cast<float*>(ws + 256 + D::ws_o_bytes(slots));
-  prm.seq_tile = reinterpret_cast<long long*>(ws + 256 + align256(D::ws_bytes(slots)));
+  prm.ws_ml = reinterpret_cast<float*>(ws + 256 + D::ws_o_bytes(slots, true));
+  prm.seq_tile = reinterpret_cast<long long*>(ws + 256 + align256(D::ws_bytes(slots, true)));
   prm.g = g;
   prm.out = out;
   prm.table = c.table;
@@ -129,7 +146,7 @@ PagedPrefillLayout paged_prefill_layout(int S, int N) {
     off = align256(off + bytes);
     return at;
   };
-  L.decode = take(hca_decode_workspace_size(N));
+  L.decode = take(hca_paged_decode_workspace_size(N));
   L.len = take(static_cast<size_t>(N) * 4);
   L.row_of = take(static_cast<size_t>(N) * 4);
   L.win_row = take(static_cast<size_t>(N) * 4);
@@ -166,7 +183,9 @@ hca_status_t hca_paged_append(const hca_bf16* k_new, const hca_bf16* v_new, cons
   if (units > 0x7fffffffLL) return HCA_ERR_UNSUPPORTED;
   G::entries_kernel<false>
       <<<dim3(static_cast<unsigned>(units), 8), G::kThreads, 0, stream>>>(ch, c, nullptr, nullptr);
-  G::finish_kernel<<<dim3(S, G::kFinishY), G::kFinishThreads, 0, stream>>>(ch, c, G::Queries{});
+  if (launch_behind(G::finish_kernel, dim3(S, G::kFinishY), G::kFinishThreads, stream, ch, c,
+                    G::Queries{}) != cudaSuccess)
+    return HCA_ERR_CUDA;
   return launch_status();
 }
 
@@ -209,7 +228,9 @@ hca_status_t hca_paged_prefill(const hca_bf16* q, const hca_bf16* g, const hca_b
   qr.gsync = reinterpret_cast<unsigned long long*>(w + L.decode);
   G::entries_kernel<true>
       <<<dim3(static_cast<unsigned>(units), 8), G::kThreads, 0, stream>>>(ch, c, raw_k, raw_v);
-  G::finish_kernel<<<dim3(S, G::kFinishY), G::kFinishThreads, 0, stream>>>(ch, c, qr);
+  if (launch_behind(G::finish_kernel, dim3(S, G::kFinishY), G::kFinishThreads, stream, ch, c, qr) !=
+      cudaSuccess)
+    return HCA_ERR_CUDA;
   hca::decode::Params prm = {};
   prm.ctx_len = qr.len;
   prm.S = N;
@@ -225,11 +246,22 @@ hca_status_t hca_paged_prefill(const hca_bf16* q, const hca_bf16* g, const hca_b
                       w + L.decode, stream);
 }
 
-hca_status_t hca_paged_decode(const hca_bf16* q, const hca_bf16* g, const int32_t* ctx_len, int S,
-                              int H, float scale, const hca_bf16* vha_down,
-                              const hca_bf16* vha_up, int vha_rank,
-                              const hca_paged_cache_t* cache, hca_bf16* out, void* ws,
-                              size_t ws_bytes, hca_stream_t stream) {
+size_t hca_paged_decode_workspace_size(int S) {
+  if (S < 1) return 0;
+  const int sms = device_sms();
+  if (sms <= 0) return 0;
+  // grid barrier counter, split partials, tile prefix
+  return 256 + align256(hca::decode::ws_bytes(sms + S, true)) + static_cast<size_t>(S + 1) * 8;
+}
+
+}  // extern "C"
+
+namespace {
+// hca_paged_decode; `step`: behind the append of its tokens, which did not write ctx_len
+hca_status_t paged_decode(const hca_bf16* q, const hca_bf16* g, const int32_t* ctx_len, int S,
+                          int H, float scale, const hca_bf16* vha_down, const hca_bf16* vha_up,
+                          int vha_rank, const hca_paged_cache_t* cache, hca_bf16* out, void* ws,
+                          size_t ws_bytes, bool step, cudaStream_t stream) {
   hca::paged::Cache c;
   hca_status_t st = attend_args(q, g, out, H, scale, vha_down, vha_up, vha_rank, ws);
   if (st != HCA_OK) return st;
@@ -237,7 +269,7 @@ hca_status_t hca_paged_decode(const hca_bf16* q, const hca_bf16* g, const int32_
   if (S > 65535) return HCA_ERR_UNSUPPORTED;
   st = paged_cache(c, cache, S, false);
   if (st != HCA_OK) return st;
-  if (ws_bytes < hca_decode_workspace_size(S)) return HCA_ERR_INVALID_ARG;
+  if (ws_bytes < hca_paged_decode_workspace_size(S)) return HCA_ERR_INVALID_ARG;
   hca::decode::Params prm = {};
   prm.ctx_len = ctx_len;
   prm.S = S;
@@ -245,8 +277,21 @@ hca_status_t hca_paged_decode(const hca_bf16* q, const hca_bf16* g, const int32_
   prm.vha_down = vha_down;
   prm.vha_up = vha_up;
   prm.vha_rank = vha_rank;
+  prm.plan_early = step ? 1 : 0;
   return paged_attend(c, q, g, out, c.wk, c.wv, static_cast<uint64_t>(S) * HCA_WINDOW, prm,
                       static_cast<uint8_t*>(ws), stream);
+}
+}  // namespace
+
+extern "C" {
+
+hca_status_t hca_paged_decode(const hca_bf16* q, const hca_bf16* g, const int32_t* ctx_len, int S,
+                              int H, float scale, const hca_bf16* vha_down,
+                              const hca_bf16* vha_up, int vha_rank,
+                              const hca_paged_cache_t* cache, hca_bf16* out, void* ws,
+                              size_t ws_bytes, hca_stream_t stream) {
+  return paged_decode(q, g, ctx_len, S, H, scale, vha_down, vha_up, vha_rank, cache, out, ws,
+                      ws_bytes, false, stream);
 }
 
 hca_status_t hca_paged_decode_step(const hca_bf16* q, const hca_bf16* g, const hca_bf16* k_new,
@@ -263,11 +308,11 @@ hca_status_t hca_paged_decode_step(const hca_bf16* q, const hca_bf16* g, const h
   if (S > 65535) return HCA_ERR_UNSUPPORTED;
   st = paged_cache(c, cache, S, true);
   if (st != HCA_OK) return st;
-  if (ws_bytes < hca_decode_workspace_size(S)) return HCA_ERR_INVALID_ARG;
+  if (ws_bytes < hca_paged_decode_workspace_size(S)) return HCA_ERR_INVALID_ARG;
   st = hca_paged_append(k_new, v_new, s_new, nullptr, ctx_len, S, S, cache, stream);
   if (st != HCA_OK) return st;
-  return hca_paged_decode(q, g, ctx_len, S, H, scale, vha_down, vha_up, vha_rank, cache, out, ws,
-                          ws_bytes, stream);
+  return paged_decode(q, g, ctx_len, S, H, scale, vha_down, vha_up, vha_rank, cache, out, ws,
+                      ws_bytes, true, stream);
 }
 
 }  // extern "C"
@@ -317,8 +362,9 @@ hca_status_t launch_move(const hca::pages::Move& m, cudaStream_t stream) {
   const long long table = (static_cast<long long>(m.rows) * m.max_pages + 1023) / 1024;
   units = units > table ? units : table;
   const long long most = 8LL * sms;
-  P::move_kernel<<<static_cast<unsigned>(units < most ? units : most), P::kMoveThreads, 0,
-                   stream>>>(m);
+  if (launch_behind(P::move_kernel, dim3(static_cast<unsigned>(units < most ? units : most)),
+                    P::kMoveThreads, stream, m) != cudaSuccess)
+    return HCA_ERR_CUDA;
   return launch_status();
 }
 

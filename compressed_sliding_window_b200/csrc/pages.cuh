@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(kPlanThreads)
                 int* __restrict__ src, int* __restrict__ dst, int* __restrict__ rsrc,
                 int* __restrict__ rdst) {
   __shared__ int red[kPlanWarps];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   // validity; dst[i] = rank of the pair's fresh page, or -1
   int fresh = 0;
@@ -295,6 +296,7 @@ __global__ void __launch_bounds__(kPlanThreads)
                    int* __restrict__ live_out) {
   __shared__ int red[kPlanWarps];
   __shared__ int live_s;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) live_s = 0;
   __syncthreads();
   int m = 0;
@@ -331,6 +333,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 __global__ void __launch_bounds__(kPlanThreads)
     check_kernel(const int* __restrict__ from, const int* __restrict__ to, int n, int items,
                  int* __restrict__ mark, int* __restrict__ src, int* __restrict__ dst) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   auto in = [&](int x) { return static_cast<unsigned>(x) < static_cast<unsigned>(items); };
   for (int i = threadIdx.x; i < n; i += kPlanThreads) {
     const int a = from[i], b = to[i];
@@ -385,6 +388,7 @@ struct Move {
 };
 
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const Move m) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the plan's lists
   const int n = m.count != nullptr ? min(*m.count, m.n) : m.n;
   if (m.table != nullptr) {
     const int live = *m.live;

@@ -414,9 +414,16 @@ hca_status_t hca_paged_prefill(const hca_bf16* q, const hca_bf16* g, const hca_b
                                void* ws, size_t ws_bytes, hca_stream_t stream);
 
 /*
+ * hca_paged_decode_workspace_size — bytes of scratch hca_paged_decode needs for
+ * S sequences, zero-filled before its first use as for hca_decode.
+ */
+size_t hca_paged_decode_workspace_size(int S);
+
+/*
  * hca_paged_decode — hca_decode (vha_rank > 0: hca_decode_vha) over a paged
  *   cache: one query per sequence, the cache already holding its token.
- *   Reads the cache only.  q, g, out [S, 64, 512]; ws as for hca_decode.
+ *   Reads the cache only.  q, g, out [S, 64, 512]; ws: at least
+ *   hca_paged_decode_workspace_size(S) bytes, one call at a time.
  * Errors:  as hca_decode_vha and hca_paged_append.
  */
 hca_status_t hca_paged_decode(const hca_bf16* q, const hca_bf16* g, const int32_t* ctx_len, int S,

@@ -375,8 +375,9 @@ def test_bad_pages_and_offsets_are_reported():
     assert hca.device_error()[0] == 5 and c.ck.isnan().all()
 
 
-def test_equals_the_contiguous_decode():
-    """Same lengths, same split, same sums: bit-identical to decode on a contiguous cache."""
+def test_agrees_with_the_contiguous_decode():
+    """Same lengths, split and sums as decode on a contiguous cache; that one also rounds the
+    split partials to bf16 (half a step of each), and both round the output."""
     need_gpu()
     gen = _gen(12)
     L = [131072, 5000, 1, 300, 128 * 77 + 5]
@@ -394,4 +395,6 @@ def test_equals_the_contiguous_decode():
     a = hca.paged_decode(q, c.ck, c.cv, c.table, c.wk, c.wv, ctx, g)
     b = hca.decode(q, ck, cv, c.wk.nan_to_num(0.0), c.wv.nan_to_num(0.0), ctx, g)
     _no_error()
-    assert torch.equal(a, b)
+    for i, x in enumerate(L):
+        ref, bound = attend64(q[i], g[i], ck[i], cv[i], seqs[i].k, seqs[i].v, x - 1)
+        assert ((a[i].double() - b[i].double()).abs() <= bound).all()
