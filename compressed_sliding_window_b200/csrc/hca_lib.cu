@@ -117,17 +117,18 @@ bool make_map_codes(CUtensorMap* m, const void* base, uint64_t Y, uint64_t Z,
 // shape).  The shared-memory attribute is a per-device property of each
 // kernel, so it is set, and the occupancy asked, once for every device the
 // process uses (with that device current).
+template <bool kPaged>
 int prefill_max_clusters() {
-  static int cached[kMaxDevices] = {};
-  static std::mutex mu;
+  static std::atomic<int> cached[kMaxDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;
-  std::lock_guard<std::mutex> lock(mu);
-  if (cached[dev] > 0) return cached[dev];
+  if (const int known = cached[dev].load(std::memory_order_acquire); known > 0) return known;
   namespace P = hca::prefill3;
-  if (cudaFuncSetAttribute(P::prefill3_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(P::prefill3_kernel<false, kPaged>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
                            P::kSmemAlloc) != cudaSuccess ||
-      cudaFuncSetAttribute(P::prefill3_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      cudaFuncSetAttribute(P::prefill3_kernel<true, kPaged>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
                            P::kSmemAlloc) != cudaSuccess)
     return -1;
   cudaLaunchConfig_t cfg = {};
@@ -142,12 +143,12 @@ int prefill_max_clusters() {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int n = 0, nv = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, P::prefill3_kernel<false>, &cfg) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&nv, P::prefill3_kernel<true>, &cfg) != cudaSuccess)
+  if (cudaOccupancyMaxActiveClusters(&n, P::prefill3_kernel<false, kPaged>, &cfg) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&nv, P::prefill3_kernel<true, kPaged>, &cfg) != cudaSuccess)
     return -1;
   n = n < nv ? n : nv;
   if (n <= 0) return -1;
-  cached[dev] = n;
+  cached[dev].store(n, std::memory_order_release);
   return n;
 }
 
@@ -252,7 +253,7 @@ hca_status_t hca_compress(const hca_bf16* k, const hca_bf16* v, const hca_bf16* 
 size_t hca_prefill_workspace_size(int B, int T) {
   if (B < 1 || T < 1) return 0;
   const long long items = static_cast<long long>(B) * ((T + 3) / 4);
-  const int max_clusters = prefill_max_clusters();
+  const int max_clusters = prefill_max_clusters<false>();
   if (max_clusters <= 0) return 0;
   const long long clusters = items < max_clusters ? items : max_clusters;
   return static_cast<size_t>(clusters) * hca::prefill3::kScratchPerCluster + 256;
@@ -282,7 +283,7 @@ hca_status_t prefill_impl(const hca_bf16* q, const hca_bf16* k, const hca_bf16* 
   const long long items = static_cast<long long>(B) * row_tiles;
   if (items > 0x7fffffffLL) return HCA_ERR_UNSUPPORTED;
 
-  const int max_clusters = prefill_max_clusters();
+  const int max_clusters = prefill_max_clusters<false>();
   if (max_clusters <= 0) return HCA_ERR_CUDA;
   const int clusters = static_cast<int>(items < max_clusters ? items : max_clusters);
   if (ws_bytes < static_cast<size_t>(clusters) * P::kScratchPerCluster) return HCA_ERR_INVALID_ARG;

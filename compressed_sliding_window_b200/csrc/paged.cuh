@@ -205,17 +205,36 @@ __global__ void __launch_bounds__(kThreads)
   (which ? cache.cv : cache.ck)[row * kD + quarter * 128 + tid] = *reinterpret_cast<uint16_t*>(&hb);
 }
 
-// What the attention reads of each query (null pointers: append alone).
+constexpr int kFinishY = 8;     // CTAs of a sequence, 16 ring slots each
+constexpr int kFinishThreads = 256;
+
+// What the attention reads beside the cache (null pointers: not wanted).
 struct Queries {
+  // one query at a time (split over the keys)
   int* len;        // [N] context length of the query
   int* row_of;     // [N] its page table row
   int* win_row;    // [N] its first window row
-  int* count;      // queries in all
   unsigned long long* gsync;   // the attention's grid barrier, reset here
+  // four positions at a time
+  int4* items;     // [cap] {table row, first packed token, its position, positions}
+  int cap;
+  int* tail16;     // [S] first entry of the last group of 16 when it is not full, or INT_MAX
+  uint16_t* tail;  // [S, 16, 512] V rows of that group, zeros behind the last entry
+  int* count;      // queries or items in all
 };
 
-constexpr int kFinishY = 8;     // CTAs of a sequence, 16 ring slots each
-constexpr int kFinishThreads = 256;
+// Sum over the CTA (kFinishThreads threads).
+__device__ __forceinline__ long long finish_sum(long long x, long long* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+  __syncthreads();
+  long long t = 0;
+  for (int w = 0; w < 8; ++w) t += red[w];
+  return t;
+}
+
 
 // grid (S, kFinishY)
 __global__ void __launch_bounds__(kFinishThreads)
@@ -225,7 +244,7 @@ __global__ void __launch_bounds__(kFinishThreads)
   const Span sp = span_of(c, i, blockIdx.y == 0 && tid == 0);
   // launched while entries_kernel may still read the rings
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (qr.count != nullptr) {
+  if (qr.len != nullptr) {
     const int base = raw_base(sp, i);
     for (int r = blockIdx.y * kFinishThreads + tid; r < sp.n; r += kFinishY * kFinishThreads) {
       qr.len[sp.qs + r] = sp.L0 + r + 1;
@@ -235,6 +254,50 @@ __global__ void __launch_bounds__(kFinishThreads)
     if (i == 0 && blockIdx.y == 0 && tid == 0) {
       *qr.count = min(max(c.q_start[c.S], 0), c.N);
       *qr.gsync = 0ull;
+    }
+  }
+  if (qr.items != nullptr) {
+    __shared__ long long red[8];
+    if (blockIdx.y == 0) {
+      // Place of this sequence's items: behind those of all sequences with a longer context
+      // (of equal ones, with a smaller number), so that the longest items are taken first.
+      long long before = 0, all = 0;
+      for (int j = tid; j < c.S; j += kFinishThreads) {
+        const Span o = span_of(c, j, false);
+        const int m = (o.n + 3) >> 2;
+        all += m;
+        if (o.L1 > sp.L1 || (o.L1 == sp.L1 && j < i)) before += m;
+      }
+      before = finish_sum(before, red);
+      const int m = (sp.n + 3) >> 2;
+      for (int r = tid; r < m; r += kFinishThreads) {
+        const long long at = before + (m - 1 - r);
+        if (at < qr.cap)   // always, unless offsets fall
+          qr.items[at] = make_int4(i, sp.qs + 4 * r, sp.L0 + 4 * r, min(4, sp.n - 4 * r));
+      }
+      if (i == 0) {
+        all = finish_sum(all, red);
+        if (tid == 0) *qr.count = static_cast<int>(min(all, static_cast<long long>(qr.cap)));
+      }
+    }
+    // the last group of 16 entries, rows 2 y and 2 y + 1
+    const int cap = cache.max_pages << cache.page_shift;
+    const int E = min(sp.L1 >> 7, cap);
+    if (blockIdx.y == 0 && tid == 0 && sp.n > 0 && (sp.L1 >> 7) - 1 > cap)
+      record_error(DEVERR_BAD_INPUT, 214);   // more entries visible than the table has room for
+    if (blockIdx.y == 0 && tid == 0) qr.tail16[i] = (E & 15) != 0 ? E & ~15 : 0x7fffffff;
+    if ((E & 15) != 0 && sp.n > 0 && tid < 128) {
+      const int r = 2 * blockIdx.y + (tid >> 6), e = (E & ~15) + r, col = (tid & 63) * 8;
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (e < E) {
+        const int pg = cache.table[i * cache.table_ld + (e >> cache.page_shift)];
+        if (static_cast<unsigned>(pg) < static_cast<unsigned>(cache.num_pages))
+          x = *reinterpret_cast<const uint4*>(
+              cache.cv +
+              ((static_cast<size_t>(pg) << cache.page_shift) + (e & ((1 << cache.page_shift) - 1))) *
+                  kD + col);
+      }
+      *reinterpret_cast<uint4*>(qr.tail + (static_cast<size_t>(i) * 16 + r) * kD + col) = x;
     }
   }
   constexpr int kSlots = kBlk / kFinishY;

@@ -134,11 +134,21 @@ hca_status_t attend_args(const hca_bf16* q, const hca_bf16* g, const hca_bf16* o
   return HCA_OK;
 }
 
+// Which form the attention of a chunk takes (measured both ways, see
+// paged_prefill).
+#ifndef HCA_SPLIT_TOKENS
+#define HCA_SPLIT_TOKENS 40
+#endif
+constexpr int kSplitTokens = HCA_SPLIT_TOKENS;
+constexpr int kMaxChunkSeqs = 4096;
+
 struct PagedPrefillLayout {
-  size_t decode, len, row_of, win_row, count, raw_k, raw_v, total;
+  bool split;   // one query at a time, split over the keys; else four positions at a time
+  int items;    // room in the item list
+  size_t decode, len, row_of, win_row, list, tail16, tail, scratch, count, raw_k, raw_v, total;
 };
 
-PagedPrefillLayout paged_prefill_layout(int S, int N) {
+PagedPrefillLayout paged_prefill_layout(int S, int N, int clusters) {
   PagedPrefillLayout L = {};
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -146,17 +156,93 @@ PagedPrefillLayout paged_prefill_layout(int S, int N) {
     off = align256(off + bytes);
     return at;
   };
-  L.decode = take(hca_paged_decode_workspace_size(N));
-  L.len = take(static_cast<size_t>(N) * 4);
-  L.row_of = take(static_cast<size_t>(N) * 4);
-  L.win_row = take(static_cast<size_t>(N) * 4);
+  L.split = N <= kSplitTokens;
+  // sum of ceil(n / 4) over S sequences with N tokens
+  L.items = static_cast<int>((static_cast<long long>(N) + 3LL * S) / 4);
   L.count = take(4);
+  if (L.split) {
+    L.decode = take(hca_paged_decode_workspace_size(N));
+    L.len = take(static_cast<size_t>(N) * 4);
+    L.row_of = take(static_cast<size_t>(N) * 4);
+    L.win_row = take(static_cast<size_t>(N) * 4);
+  } else {
+    L.list = take(static_cast<size_t>(L.items) * 16);
+    L.tail16 = take(static_cast<size_t>(S) * 4);
+    L.tail = take(static_cast<size_t>(S) * 16 * HCA_HEAD_DIM * 2);
+    L.scratch = take(static_cast<size_t>(clusters) * hca::prefill3::kScratchPerCluster);
+  }
   const size_t raw = (static_cast<size_t>(N) + static_cast<size_t>(hca::paged::kPad) * S) *
                      HCA_HEAD_DIM * 2;
   L.raw_k = take(raw);
   L.raw_v = take(raw);
   L.total = off;
   return L;
+}
+
+// Four positions at a time: the prefill kernel over the item list in `w`.
+hca_status_t paged_items(const hca::paged::Cache& c, const PagedPrefillLayout& L, uint8_t* w,
+                         const hca_bf16* q, const hca_bf16* g, hca_bf16* out, int S, int N,
+                         float scale, const hca_bf16* vha_down, const hca_bf16* vha_up,
+                         int vha_rank, int clusters, cudaStream_t stream) {
+  namespace P = hca::prefill3;
+  P::PagedMaps maps;
+  const uint64_t rows = static_cast<uint64_t>(N) * HCA_NUM_HEADS;
+  const uint64_t raw = static_cast<uint64_t>(N) + static_cast<uint64_t>(hca::paged::kPad) * S;
+  const uint64_t prows = static_cast<uint64_t>(clusters) * P::kScratchPerCluster / 256;
+  const uint32_t page = 1u << c.page_shift;
+  bool ok = make_map4(&maps.q4, q, rows, 1, 128, 4) && make_map4(&maps.g4, g, rows, 1, 128, 2) &&
+            make_map4(&maps.out4, out, rows, 1, 128, 2) &&
+            make_map4(&maps.out1, out, rows, 1, 64, 1) &&
+            make_map(&maps.kwin, w + L.raw_k, HCA_HEAD_DIM, raw, 1, P::kWinHalf) &&
+            make_map4(&maps.v4, w + L.raw_v, raw, 1, 128, 2) &&
+            make_map4(&maps.v4t, w + L.raw_v, raw, 1, 16, 1) &&
+            make_map4(&maps.tail, w + L.tail, static_cast<uint64_t>(S) * 16, 1, 16, 1) &&
+            make_map_bytes(&maps.p128, w + L.scratch, prows, 128) &&
+            make_map_bytes(&maps.p16, w + L.scratch, prows, 16);
+  if (ok && c.num_pages > 0) {
+    ok = make_map(&maps.ck, c.ck, HCA_HEAD_DIM, page, c.num_pages, page < 64 ? page : 64) &&
+         make_map4(&maps.cv4, c.cv, page, c.num_pages, page, 1) &&
+         make_map4(&maps.cv16, c.cv, page, c.num_pages, 16, 1);
+  } else if (ok) {   // no entry can be visible: never used
+    maps.ck = maps.kwin;
+    maps.cv4 = maps.cv16 = maps.v4t;
+  }
+  if (!ok) return HCA_ERR_CUDA;
+  P::Params prm = {};
+  prm.scale_log2 = scale * 1.4426950408889634f;
+  prm.pscratch = w + L.scratch;
+  prm.vha_down = vha_down;
+  prm.vha_up = vha_up;
+  prm.vha_rank = vha_rank;
+  prm.item_list = reinterpret_cast<const int4*>(w + L.list);
+  prm.item_count = reinterpret_cast<const int*>(w + L.count);
+  prm.tail16 = reinterpret_cast<const int*>(w + L.tail16);
+  prm.table = c.table;
+  prm.table_ld = c.table_ld;
+  prm.num_pages = c.num_pages;
+  prm.page_shift = c.page_shift;
+  prm.max_nc = c.num_pages > 0 ? c.max_pages << c.page_shift : 0;
+  prm.raw_pad = hca::paged::kPad;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(4 * clusters);
+  cfg.blockDim = dim3(P::kThreads);
+  cfg.dynamicSmemBytes = P::kSmemAlloc;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err = vha_rank > 0
+                              ? cudaLaunchKernelEx(&cfg, P::prefill3_kernel<true, true>, maps, prm)
+                              : cudaLaunchKernelEx(&cfg, P::prefill3_kernel<false, true>, maps, prm);
+  return err == cudaSuccess ? launch_status() : HCA_ERR_CUDA;
+}
+
+// clusters of the prefill kernel for at most `items` items
+int paged_clusters(int items) {
+  const int most = prefill_max_clusters<true>();
+  return items < most ? items : most;
 }
 
 }  // namespace
@@ -190,8 +276,13 @@ hca_status_t hca_paged_append(const hca_bf16* k_new, const hca_bf16* v_new, cons
 }
 
 size_t hca_paged_prefill_workspace_size(int S, int N) {
-  if (S < 1 || N < 1 || device_sms() <= 0) return 0;
-  return paged_prefill_layout(S, N).total;
+  if (S < 1 || N < 1) return 0;
+  const int clusters = paged_clusters(0x7fffffff);
+  if (clusters <= 0) return 0;
+  // no smaller for fewer tokens: one workspace serves every call of at most S and N
+  const size_t a = paged_prefill_layout(S, N < kSplitTokens ? N : kSplitTokens, clusters).total;
+  const size_t b = N > kSplitTokens ? paged_prefill_layout(S, N, clusters).total : 0;
+  return a > b ? a : b;
 }
 
 hca_status_t hca_paged_prefill(const hca_bf16* q, const hca_bf16* g, const hca_bf16* k_new,
@@ -211,26 +302,38 @@ hca_status_t hca_paged_prefill(const hca_bf16* q, const hca_bf16* g, const hca_b
   st = paged_cache(c, cache, S, true);
   if (st != HCA_OK) return st;
   if (N == 0) return HCA_OK;
-  const long long units = entry_units(S, N);
-  if (S > 65535 || static_cast<long long>(N) + static_cast<long long>(G::kPad) * S >
-                       0x7fffffffLL / HCA_NUM_HEADS)
+  if (S > kMaxChunkSeqs || static_cast<long long>(N) + static_cast<long long>(G::kPad) * S >
+                               0x7fffffffLL / HCA_NUM_HEADS)
     return HCA_ERR_UNSUPPORTED;
-  const PagedPrefillLayout L = paged_prefill_layout(S, N);
+  const long long units = entry_units(S, N);
+  const int most = prefill_max_clusters<true>();
+  if (most <= 0) return HCA_ERR_CUDA;
+  const PagedPrefillLayout L = paged_prefill_layout(S, N, most);
   if (ws_bytes < L.total) return HCA_ERR_INVALID_ARG;
   uint8_t* w = static_cast<uint8_t*>(ws);
   uint16_t* raw_k = reinterpret_cast<uint16_t*>(w + L.raw_k);
   uint16_t* raw_v = reinterpret_cast<uint16_t*>(w + L.raw_v);
-  G::Queries qr;
-  qr.len = reinterpret_cast<int*>(w + L.len);
-  qr.row_of = reinterpret_cast<int*>(w + L.row_of);
-  qr.win_row = reinterpret_cast<int*>(w + L.win_row);
+  G::Queries qr = {};
   qr.count = reinterpret_cast<int*>(w + L.count);
-  qr.gsync = reinterpret_cast<unsigned long long*>(w + L.decode);
+  if (L.split) {
+    qr.len = reinterpret_cast<int*>(w + L.len);
+    qr.row_of = reinterpret_cast<int*>(w + L.row_of);
+    qr.win_row = reinterpret_cast<int*>(w + L.win_row);
+    qr.gsync = reinterpret_cast<unsigned long long*>(w + L.decode);
+  } else {
+    qr.items = reinterpret_cast<int4*>(w + L.list);
+    qr.cap = L.items;
+    qr.tail16 = reinterpret_cast<int*>(w + L.tail16);
+    qr.tail = reinterpret_cast<uint16_t*>(w + L.tail);
+  }
   G::entries_kernel<true>
       <<<dim3(static_cast<unsigned>(units), 8), G::kThreads, 0, stream>>>(ch, c, raw_k, raw_v);
   if (launch_behind(G::finish_kernel, dim3(S, G::kFinishY), G::kFinishThreads, stream, ch, c, qr) !=
       cudaSuccess)
     return HCA_ERR_CUDA;
+  if (!L.split)
+    return paged_items(c, L, w, q, g, out, S, N, scale, vha_down, vha_up, vha_rank,
+                       paged_clusters(L.items), stream);
   hca::decode::Params prm = {};
   prm.ctx_len = qr.len;
   prm.S = N;

@@ -50,6 +50,19 @@
 // of value half 1 is issued after the next item's first P.V stages of value
 // half 0, so that waiting for it never holds those back.
 //
+// Paged cache (kPaged).  The items come from a list in the workspace, 4
+// positions of one sequence each, the longest contexts first; packed token
+// rows address q, g and out, and the raw keys of a sequence lie in rows of the
+// workspace that hold its last 127 tokens, the chunk and zeros, so the raw
+// tile is loaded as in the contiguous case.  Compressed tiles are loaded page
+// by page, one box per lane of the producer warps; the S width of a tile is
+// rounded up to a whole box for each CTA of the pair, its P and V width to 16
+// keys.  Only the last group of 16 entries of a sequence can hold rows that
+// belong to no entry (and may be NaN, which 0 probabilities would not stop):
+// its V rows are loaded from a copy in the workspace with zeros behind the
+// last entry.  An item of fewer than 4 positions stores row by row of
+// positions, so the rows of the next sequence stay as they are.
+//
 // Warp roles (544 threads): warps 0-1 TMA producers, warp 2 TMEM owner and (in
 // even CTAs) MMA issuer, warps 3-10 compute: two warps per TMEM lane quadrant.
 // On S-CTAs each owns one 128-key half of the score rows; on O-CTAs they
@@ -57,6 +70,8 @@
 // warp 11 (P copier), warp 12 (output stores) and warps 13-16 (epilogue of
 // value columns 256-511).
 #pragma once
+
+#include <type_traits>
 
 #include "hca_ptx.cuh"
 
@@ -135,6 +150,15 @@ struct Params {
   const uint16_t* vha_down;   // VHA factors [64][vha_rank] bf16 (kVha only)
   const uint16_t* vha_up;
   int vha_rank;
+  // kPaged only
+  const int4* item_list;      // {table row, first packed token, its position, positions}
+  const int* item_count;
+  const int* tail16;          // [S] first entry of the copied group, or INT_MAX
+  const int* table;           // row r at table + r * table_ld
+  long long table_ld;
+  int num_pages, page_shift;
+  int max_nc;                 // entries the table has room for
+  int raw_pad;                // raw rows of a sequence beyond its tokens
 };
 
 struct Maps {
@@ -149,16 +173,40 @@ struct Maps {
   CUtensorMap p128;  // P scratch as [rows of 256 B], box (256, 128): one 32 KB slot
   CUtensorMap p16;   // same, box (256, 16): the first 16 keys of a slot
 };
+// kPaged: q4, g4, out4 with T = all packed tokens, B = 1; kwin, v4, v4t over the
+// raw rows; ck [pages][P][512], box (64, min(P, 64), 1); cv4 (64, P, 8, pages),
+// box (64, P, 1, 1); and
+struct PagedMaps : Maps {
+  CUtensorMap cv16;   // cv4 with boxes of 16 rows
+  CUtensorMap tail;   // (64, 16 S, 8, 1), box (64, 16, 1, 1): copied last groups
+  CUtensorMap out1;   // (64, T*64, 8, 1), box (64, 64, 1, 1): one slab of one position
+};
 
 __device__ __forceinline__ int nc_of(int t) { return t >= 127 ? (t - 127) / 128 : 0; }
 
 struct Item {
   int b, t0, np;      // batch, first position, valid positions (1..4)
   int ncmax, n_ctiles, ntiles;
+  int tok, raw;       // row of the first position in q, g and out, and of raw key t0 - 127
+  int seq;            // kPaged: table row
 };
 
+template <bool kPaged>
 __device__ __forceinline__ Item decode_item(const Params& p, int it) {
   Item x;
+  if constexpr (kPaged) {
+    const int4 e = p.item_list[it];
+    x.b = 0;
+    x.seq = e.x;
+    x.tok = e.y;
+    x.t0 = e.z;
+    x.np = e.w;
+    x.raw = x.tok + p.raw_pad * x.seq;
+    x.ncmax = min(nc_of(x.t0 + x.np - 1), p.max_nc);
+    x.n_ctiles = (x.ncmax + kKT - 1) / kKT;
+    x.ntiles = x.n_ctiles + 1;
+    return x;
+  }
   const int rank = it / p.B;
   x.b = it - rank * p.B;
   x.t0 = kPos * (p.row_tiles - 1 - rank);
@@ -166,6 +214,9 @@ __device__ __forceinline__ Item decode_item(const Params& p, int it) {
   x.ncmax = nc_of(x.t0 + x.np - 1);
   x.n_ctiles = (x.ncmax + kKT - 1) / kKT;
   x.ntiles = x.n_ctiles + 1;
+  x.tok = x.t0;
+  x.raw = x.t0 - 127;
+  x.seq = 0;
   return x;
 }
 
@@ -173,6 +224,23 @@ __device__ __forceinline__ Item decode_item(const Params& p, int it) {
 __device__ __forceinline__ int tile_n(const Item& x, int j) {
   if (j < x.n_ctiles) return (min(kKT, x.ncmax - j * kKT) + 15) & ~15;
   return kWinN;
+}
+// width of S of key tile j: with pages each CTA of the pair loads whole boxes of
+// min(P, 64) entries
+template <bool kPaged>
+__device__ __forceinline__ int tile_s(const Params& p, const Item& x, int j) {
+  const int n = tile_n(x, j);
+  if (!kPaged || j >= x.n_ctiles) return n;
+  const int r2 = 2 << min(p.page_shift, 6);
+  return (n + r2 - 1) & ~(r2 - 1);
+}
+// page that holds entry e of an item's sequence; a page number outside of the
+// pool (reported) becomes one past the last, whose boxes are filled with zeros
+__device__ __forceinline__ int page_of(const Params& p, const Item& x, int e) {
+  const int pg = p.table[x.seq * p.table_ld + (e >> p.page_shift)];
+  if (static_cast<unsigned>(pg) < static_cast<unsigned>(p.num_pages)) return pg;
+  record_error(DEVERR_BAD_INPUT, 301);
+  return p.num_pages;
 }
 // keys of sub-tile h (0: columns 0..127, 1: columns 128..) of a tile of width n
 __device__ __forceinline__ int sub_n(int n, int h) { return h == 0 ? min(n, 128) : max(0, n - 128); }
@@ -219,9 +287,10 @@ __device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int x, i
                : "memory");
 }
 
-template <bool kVha>
+template <bool kVha, bool kPaged = false>
 __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
-    prefill3_kernel(const __grid_constant__ Maps maps, const Params p) {
+    prefill3_kernel(const __grid_constant__ std::conditional_t<kPaged, PagedMaps, Maps> maps,
+                    const Params p) {
   constexpr int NV = kVha ? kVStagesVha : kVStages;   // V ring stages
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
@@ -287,6 +356,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
   }
   cluster_sync_all();  // every CTA's barriers exist before any remote access
   tc_fence_after();
+  // launched while the kernel that writes the item list may still run
+  if constexpr (kPaged) asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int items = kPaged ? *p.item_count : p.items;
   const uint32_t tmem = *tmem_slot;
 
   if (!isO) {
@@ -295,14 +367,70 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     // =====================================================================
     if (warp <= 1) {
       // --------------------------------------------------------- producers
-      if (lane == 0) {
+      if constexpr (kPaged) {
+        // lane 0 waits and loads what is one box; lane 8 s + r loads box r of slab s of a
+        // compressed half (up to 8 boxes of one page each)
+        const int me = warp;
+        const int rsh = min(p.page_shift, 6);      // log2(entries of a box)
+        const int bx = lane & 7, slab = lane >> 3;
+        uint32_t u = 0, nitem = 0;
+        bool ok = true;
+        for (int it = cluster; it < items && ok; it += nclusters, ++nitem) {
+          const Item x = decode_item<kPaged>(p, it);
+          if (lane == 0) {
+            if (me == 0 && it + nclusters < items) {
+              const Item y = decode_item<kPaged>(p, it + nclusters);
+              tma_prefetch_4d(&maps.q4, 0, (y.tok + 2 * half) * kHeads, 0, 0);
+              tma_prefetch_4d(&maps.q4, 0, (y.tok + 2 * half) * kHeads, 4, 0);
+            }
+            ok = mbar_wait(bar(QEMPTY + me), (nitem & 1) ^ 1, abort_flag, kWaitLimitNs, 310);
+            if (ok) {
+              if (leader) mbar_expect_tx(bar(QFULL + me), 2 * kQHalf);
+              tma_load_4d_pair(sb + S_Q + me * kQHalf, &maps.q4, lbar(QFULL + me), 0,
+                               (x.tok + 2 * half) * kHeads, 4 * me, 0);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          for (int j = 0; j < x.ntiles && ok; ++j) {
+            const bool comp = j < x.n_ctiles;
+            const int valid = comp ? min(kKT, x.ncmax - j * kKT) : 0;   // entries of the tile
+            const int first = half * (tile_s<kPaged>(p, x, j) >> 1) + (bx << rsh);
+            const bool mine = comp && slab < 2 && (bx << rsh) < (tile_s<kPaged>(p, x, j) >> 1) &&
+                              first < valid;
+            const int e = j * kKT + first;
+            const int pg = mine ? page_of(p, x, e) : 0;
+            const uint32_t bytes =
+                comp ? 2u * (((valid + (1 << rsh) - 1) >> rsh) << rsh) * 128u : 2u * 2u * kWinHalf * 128u;
+            for (int d2 = 0; d2 < 4 && ok; ++d2, ++u) {
+              if ((u & 1) != static_cast<uint32_t>(me)) continue;
+              const uint32_t st = u % kKStages;
+              const uint32_t dst = sb + S_KRING + st * kKStage;
+              const uint32_t fb = lbar(KFULL + st);
+              if (lane == 0) {
+                ok = mbar_wait(bar(KEMPTY + st), ((u / kKStages) & 1) ^ 1, abort_flag, kWaitLimitNs,
+                               311);
+                if (ok && leader) mbar_expect_tx(bar(KFULL + st), bytes);
+              }
+              ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+              __syncwarp();
+              if (!ok) break;
+              if (mine)
+                tma_load_3d_pair(dst + slab * kKSlab + (bx << rsh) * 128, &maps.ck, fb,
+                                 64 * (2 * d2 + slab), e & ((1 << p.page_shift) - 1), pg);
+              if (!comp && bx == 0 && slab < 2)
+                tma_load_3d_pair(dst + slab * kKSlab, &maps.kwin, fb, 64 * (2 * d2 + slab),
+                                 x.raw + half * kWinHalf, 0);
+            }
+          }
+        }
+      } else if (lane == 0) {
         const int me = warp;
         uint32_t u = 0, nitem = 0;
         bool ok = true;
-        for (int it = cluster; it < p.items && ok; it += nclusters, ++nitem) {
-          const Item x = decode_item(p, it);
-          if (me == 0 && it + nclusters < p.items) {  // warm L2 with the next item's Q rows
-            const Item y = decode_item(p, it + nclusters);
+        for (int it = cluster; it < items && ok; it += nclusters, ++nitem) {
+          const Item x = decode_item<kPaged>(p, it);
+          if (me == 0 && it + nclusters < items) {  // warm L2 with the next item's Q rows
+            const Item y = decode_item<kPaged>(p, it + nclusters);
             tma_prefetch_4d(&maps.q4, 0, (y.t0 + 2 * half) * kHeads, 0, y.b);
             tma_prefetch_4d(&maps.q4, 0, (y.t0 + 2 * half) * kHeads, 4, y.b);
           }
@@ -350,13 +478,14 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       if (leader && lane == 0) {
         uint32_t u = 0, sj = 0, nitem = 0;
         bool ok = true;
-        for (int it = cluster; it < p.items && ok; it += nclusters, ++nitem) {
-          const Item x = decode_item(p, it);
+        for (int it = cluster; it < items && ok; it += nclusters, ++nitem) {
+          const Item x = decode_item<kPaged>(p, it);
           for (int j = 0; j < x.ntiles && ok; ++j, ++sj) {
             const uint32_t buf = sj & 1;
             ok &= mbar_wait_cluster(bar(SFREE + buf), ((sj >> 1) & 1) ^ 1, abort_flag,
                                     kWaitLimitNs, 320);
-            const uint32_t idesc = idesc_bf16_f32(2 * kRows, tile_n(x, j), false, false);
+            const uint32_t idesc =
+                idesc_bf16_f32(2 * kRows, tile_s<kPaged>(p, x, j), false, false);
             const uint32_t dS = tmem + 256 * buf;
             const bool first = j == 0, last = j + 1 == x.ntiles;
 #pragma unroll 1
@@ -429,10 +558,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_cluster(peerPReady + 8 * (pend - 1));
         pend = 0;
       };
-      for (int it = cluster; it < p.items; it += nclusters, ++nitem) {
-        const Item x = decode_item(p, it);
+      for (int it = cluster; it < items; it += nclusters, ++nitem) {
+        const Item x = decode_item<kPaged>(p, it);
         const int t = x.t0 + pos;
-        const int ncp = nc_of(min(t, p.T - 1));
+        const int ncp = kPaged ? min(nc_of(t), x.ncmax) : nc_of(min(t, p.T - 1));
         float m = -INFINITY, l = 0.f;
         for (int j = 0; j < x.ntiles; ++j, ++sj) {
           const uint32_t buf = sj & 1;
@@ -562,7 +691,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
           st_cluster_b32(peerInvl + 4 * row, __float_as_uint(1.f / l));
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(peerStatsFull);
-          if (p.lse != nullptr && t < p.T)
+          if (!kPaged && p.lse != nullptr && t < p.T)
             p.lse[(static_cast<size_t>(x.b) * p.T + t) * kHeads + (row & 63)] =
                 (m + __log2f(l)) * 0.6931471805599453f;
         }
@@ -581,12 +710,97 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     const int orow0 = 2 * half;   // first position of this CTA's rows
     if (warp <= 1) {
       // --------------------------------------------------------- producers
-      if (lane == 0) {
+      if constexpr (kPaged) {
+        // as on the S-CTAs: lane 8 s + r loads box r of slab s
+        const int me = warp;
+        const int bx = lane & 7, slab = lane >> 3;
+        uint32_t u = 0;
+        bool ok = true;
+        for (int it = cluster; it < items && ok; it += nclusters) {
+          const Item x = decode_item<kPaged>(p, it);
+          const int tail = p.tail16[x.seq];
+          if (me == 0 && lane < 4)
+            tma_prefetch_4d(&maps.g4, 0, (x.tok + orow0) * kHeads, 2 * lane, 0);
+          for (int j = 0; j < x.ntiles && ok; ++j) {
+            const int n = tile_n(x, j);
+            const bool comp = j < x.n_ctiles;
+            const bool two = sub_n(n, 1) > 0;
+            const int nst = two ? 4 : 2;
+            // this lane's box of the two sub-tiles: rows of a box, entries, page
+            int rsh[2], e[2], pg[2];
+            uint32_t bytes[2];
+            bool mine[2], cop[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int nh = comp ? sub_n(n, h) : 0;      // multiple of 16
+              const int e0 = j * kKT + 128 * h;
+              const bool last = e0 + nh > tail;           // holds the copied group
+              rsh[h] = last ? 4 : p.page_shift;
+              const int first = bx << rsh[h];
+              mine[h] = slab < 2 && first < nh;
+              e[h] = e0 + first;
+              cop[h] = last && e[h] == tail;
+              pg[h] = mine[h] && !cop[h] ? page_of(p, x, e[h]) : 0;
+              bytes[h] = 2u * 2u * (((nh + (1 << rsh[h]) - 1) >> rsh[h]) << rsh[h]) * 128u;
+            }
+            for (int s = 0; s < nst && ok; ++s, ++u) {
+              if ((u & 1) != static_cast<uint32_t>(me)) continue;
+              int dh, h;
+              pv_stage(s, two, j == 0 || j == x.ntiles - 1, dh, h);
+              const uint32_t st = u % NV;
+              const uint32_t fb = lbar(VFULL + st);
+              const bool wtail = !comp && h == 1;          // raw keys t0 + 1 .. t0 + 16
+              if (lane == 0) {
+                ok = mbar_wait(bar(VEMPTY + st), ((u / NV) & 1) ^ 1, abort_flag, kWaitLimitNs, 340);
+                if (ok && leader)
+                  mbar_expect_tx(bar(VFULL + st), comp    ? (h ? bytes[1] : bytes[0])
+                                                  : wtail ? 2u * 2u * 16u * 128u
+                                                          : 2u * 2u * 128u * 128u);
+              }
+              ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+              __syncwarp();
+              if (!ok) break;
+              const uint32_t dst = sb + O_VRING + st * kVStage;
+              const int z = 4 * dh + 2 * half;
+              if (comp) {
+                if (h ? mine[1] : mine[0]) {
+                  const int sh = h ? rsh[1] : rsh[0], ee = h ? e[1] : e[0];
+                  const bool cp = h ? cop[1] : cop[0];
+                  tma_load_4d_pair(dst + slab * 16384 + (bx << sh) * 128,
+                                   cp                   ? &maps.tail
+                                   : sh == p.page_shift ? &maps.cv4
+                                                        : &maps.cv16,
+                                   fb, 0, cp ? 16 * x.seq : ee & ((1 << p.page_shift) - 1),
+                                   z + slab, cp ? 0 : (h ? pg[1] : pg[0]));
+                }
+              } else if (wtail) {
+                if (bx == 0 && slab < 2)
+                  tma_load_4d_pair(dst + slab * 16384, &maps.v4t, fb, 0, x.raw + 128, z + slab, 0);
+              } else if (lane == 0) {
+                tma_load_4d_pair(dst, &maps.v4, fb, 0, x.raw, z, 0);
+              }
+            }
+          }
+          for (int g = 0; g < 4 && ok; ++g, ++u) {   // gate stages of this CTA's rows
+            if ((u & 1) != static_cast<uint32_t>(me)) continue;
+            const uint32_t st = u % NV;
+            if (lane == 0) {
+              ok = mbar_wait(bar(VEMPTY + st), ((u / NV) & 1) ^ 1, abort_flag, kWaitLimitNs, 341);
+              if (ok) {
+                mbar_expect_tx(bar(GFULL + st), kVStage);
+                tma_load_4d(sb + O_VRING + st * kVStage, &maps.g4, bar(GFULL + st), 0,
+                            (x.tok + orow0) * kHeads, 2 * g, 0);
+              }
+            }
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          }
+        }
+      } else if (lane == 0) {
         const int me = warp;
         uint32_t u = 0;
         bool ok = true;
-        for (int it = cluster; it < p.items && ok; it += nclusters) {
-          const Item x = decode_item(p, it);
+        for (int it = cluster; it < items && ok; it += nclusters) {
+          const Item x = decode_item<kPaged>(p, it);
           if (me == 0) {  // warm L2 with this item's gate rows; they are staged after its V
 #pragma unroll 1
             for (int e = 0; e < 4; ++e)
@@ -642,8 +856,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         const int prow0 = ((cluster * 2 + half) * 4) * (kSlot / 256);  // first 256-B row of my slots
         uint32_t sj = 0;
         bool ok = true;
-        for (int it = cluster; it < p.items && ok; it += nclusters) {
-          const Item x = decode_item(p, it);
+        for (int it = cluster; it < items && ok; it += nclusters) {
+          const Item x = decode_item<kPaged>(p, it);
           for (int j = 0; j < x.ntiles && ok; ++j, ++sj) {
             const int n = tile_n(x, j);
 #pragma unroll 1
@@ -672,8 +886,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         uint32_t ubase = 0, nitem = 0;
         bool ok = true;
-        for (int it = cluster; it < p.items && ok; it += nclusters, ++nitem) {
-          const Item x = decode_item(p, it);
+        for (int it = cluster; it < items && ok; it += nclusters, ++nitem) {
+          const Item x = decode_item<kPaged>(p, it);
           const uint32_t gbase = ubase + v_uses(x);
           ubase = gbase + 4;
 #pragma unroll 1
@@ -681,8 +895,19 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t st = (gbase + e) % NV;
             ok = mbar_wait(bar(STAGED + e), nitem & 1, abort_flag, kWaitLimitNs, 370);
             if (!ok) break;
-            tma_store_4d(&maps.out4, sb + O_VRING + st * kVStage, 0, (x.t0 + orow0) * kHeads,
-                         2 * e, x.b);
+            if constexpr (kPaged) {
+              const uint32_t src = sb + O_VRING + st * kVStage;
+              const int y = (x.tok + orow0) * kHeads;
+              if (x.np >= orow0 + 2) {
+                tma_store_4d(&maps.out4, src, 0, y, 2 * e, 0);
+              } else if (x.np == orow0 + 1) {   // one position: the next row is another's
+                tma_store_4d(&maps.out1, src, 0, y, 2 * e, 0);
+                tma_store_4d(&maps.out1, src + 16384, 0, y, 2 * e + 1, 0);
+              }
+            } else {
+              tma_store_4d(&maps.out4, sb + O_VRING + st * kVStage, 0, (x.t0 + orow0) * kHeads,
+                           2 * e, x.b);
+            }
             bulk_commit();
             if (e & 1) {
               // both stages of this value half are in flight: release them as
@@ -745,8 +970,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
           }
           return true;
         };
-        for (int it = cluster; it < p.items && ok; it += nclusters, ++nitem) {
-          const Item x = decode_item(p, it);
+        for (int it = cluster; it < items && ok; it += nclusters, ++nitem) {
+          const Item x = decode_item<kPaged>(p, it);
           for (int j = 0; j < x.ntiles && ok; ++j, ++sj) {
             const int n = tile_n(x, j);
             if (j > 0)  // an item's first tile never needs a rescale of O
@@ -830,8 +1055,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t partnerStatsFree = mapa_shared(bar(STATSFREE), rank - 2);
       uint32_t sj = 0, nitem = 0, ubase = 0, ncorr = 0, gpar = 0;
       bool ok = true;
-      for (int it = cluster; it < p.items && ok; it += nclusters, ++nitem) {
-        const Item x = decode_item(p, it);
+      for (int it = cluster; it < items && ok; it += nclusters, ++nitem) {
+        const Item x = decode_item<kPaged>(p, it);
         ++sj;  // the first tile of an item needs no correction
         for (int j = 1; j < x.ntiles && !helper; ++j, ++sj, ++ncorr) {
           if (!mbar_wait_cluster_warp(bar(PREADY + (sj & 1) * 2), (sj >> 1) & 1, abort_flag,

@@ -384,7 +384,8 @@ hca_status_t hca_paged_append(const hca_bf16* k_new, const hca_bf16* v_new, cons
 
 /*
  * hca_paged_prefill_workspace_size — bytes of scratch hca_paged_prefill needs
- * for S sequences with N new tokens in all.  Returns 0 for S < 1 or N < 1.
+ * for up to S sequences with up to N new tokens in all.  Returns 0 for S < 1
+ * or N < 1 or when the device cannot be asked.
  */
 size_t hca_paged_prefill_workspace_size(int S, int N);
 
@@ -404,7 +405,7 @@ size_t hca_paged_prefill_workspace_size(int S, int N);
  *          outputs of up to 16 positions before it in its sequence, and
  *          nothing else's.
  * Errors:  those of hca_paged_append (q_start is required), of hca_decode_vha,
- *          and HCA_ERR_UNSUPPORTED for S > 65535 or (N + 144 S) * 64 >= 2^31.
+ *          and HCA_ERR_UNSUPPORTED for S > 4096 or (N + 144 S) * 64 >= 2^31.
  */
 hca_status_t hca_paged_prefill(const hca_bf16* q, const hca_bf16* g, const hca_bf16* k_new,
                                const hca_bf16* v_new, const hca_bf16* s_new,
