@@ -38,18 +38,6 @@
 // P.V (the row sums use the unscaled probabilities), so no scaling touches
 // the operand tiles.
 //
-// Paged cache (decode_kernel<.., true>).  The entries of a query's sequence lie
-// in pages of 16, 32, 64 or 128 entries named by a page table, and the queries
-// need not be one per sequence: query s reads table row row_of[s] and the 128
-// window rows from win_row[s] on.  A 32 KB stage is brought by one box per
-// page (and 64-wide slab), issued by as many lanes of the producer warp; each
-// lane keeps the page number of its box in a register, read one tile ahead.
-// Boxes past the last visible entry use a page number outside the pool, which
-// fills their rows with zeros.  The rows of the last page behind the last
-// visible entry may hold anything: their scores are replaced by -inf, P.V
-// stops at the next multiple of 16 keys, and the MMA warp clears the (at most
-// 15) V rows up to there, because 0 x NaN would reach the sums otherwise.
-//
 // The softmax runs across lanes: each thread owns one key and its 64 head scores, and the
 // per-head max / sum over the 128 keys come from a shuffle transpose-reduce
 // (62 shuffles per warp) plus one small shared-memory step.
@@ -112,16 +100,11 @@ constexpr uint32_t kTmemO = 0, kTmemS0 = 256, kTmemS1 = 320, kTmemCols = 512;
 // l and stored with value column 128c + r at [r][c] (one 8-byte store per head
 // and TMEM lane); then [slots][2][64] fp32 (m, l)
 // in log2 units.  slots = grid + S.
-// Paged cache: [slots][64 heads][512] fp32 partial O, columns in order.  In
-// bf16 the partials' rounding adds in squares to that of the probabilities and
-// of the output (each 2^-8 at most): 2.8e-3 off the 64-bit result, 2.3e-3 with
-// fp32 partials (relative 2-norm, 64 x 131072 tokens), for 66 KB more per slot
-// through L2.
-__host__ __device__ inline size_t ws_o_bytes(int slots, bool f32 = false) {
-  return static_cast<size_t>(slots) * kHeads * kDim * (f32 ? 4 : 2);
+__host__ __device__ inline size_t ws_o_bytes(int slots) {
+  return static_cast<size_t>(slots) * kHeads * kDim * 2;
 }
-__host__ __device__ inline size_t ws_bytes(int slots, bool f32 = false) {
-  return ws_o_bytes(slots, f32) + static_cast<size_t>(slots) * 2 * kHeads * 4;
+__host__ __device__ inline size_t ws_bytes(int slots) {
+  return ws_o_bytes(slots) + static_cast<size_t>(slots) * 2 * kHeads * 4;
 }
 
 struct Params {
@@ -129,7 +112,7 @@ struct Params {
   int S;
   int max_nc;
   float scale_log2;
-  uint16_t* ws_o;      // [slots][64][128][4] bf16 (paged cache: [slots][64][512] fp32)
+  uint16_t* ws_o;      // [slots][64][128][4] bf16
   float* ws_ml;        // [slots][2][64]
   long long* seq_tile; // [S + 1] exclusive prefix of tile counts (plan kernel, S > kInlineSeqs)
   unsigned long long* gsync;  // grid barrier arrivals (zero before first use, see below)
@@ -144,15 +127,6 @@ struct Params {
   const uint16_t* vha_down;
   const uint16_t* vha_up;
   int vha_rank;
-  // paged cache only (decode_kernel<.., true>)
-  const int* table;    // page table, row r at table + r * table_ld
-  long long table_ld;
-  int num_pages;
-  int page_shift;      // log2(entries per page)
-  const int* row_of;   // [S] table row of each query, null: query s has row s
-  const int* win_row;  // [S] first window row of each query, null: a ring at 128 s
-  const int* count;    // number of queries on the device (at most S), null: S
-  int plan_early;      // ctx_len is older than the kernel in front: plan before waiting for it
 };
 
 __device__ __forceinline__ int nc_of_len(int L) { return L >= 128 ? (L - 128) / 128 : 0; }
@@ -169,10 +143,8 @@ __device__ __forceinline__ long long div_nn(long long a, long long b) {
 // Plan: tile counts per sequence and their exclusive prefix (one CTA).
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ ctx_len, int S,
-                                                    int max_nc, long long* __restrict__ seq_tile,
-                                                    const int* __restrict__ count) {
+                                                    int max_nc, long long* __restrict__ seq_tile) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (count != nullptr) S = min(max(*count, 0), S);
   __shared__ long long carry;
   __shared__ long long wsum[32];
   if (threadIdx.x == 0) carry = 0;
@@ -294,9 +266,6 @@ __device__ __forceinline__ void inline_plan(const Params& p, long long* sT, int*
 // (64, rows, n, 1) lands as n 64-wide slabs of [rows][64], 128B-swizzled.
 // (FP8 cache: ck, cv, wk, wv are [S][rows][512 bytes] code maps, box
 // (128 bytes, 128 rows, 1), no swizzle.)
-// Paged: ck, cv are (64, page, 8, pages) maps with boxes of one page and one
-// slab (codes: [pages][page][512 bytes], box (128 bytes, page, 1)); wk, wv are
-// one [rows][512] tensor.
 struct Maps {
   CUtensorMap q;    // (64, S*64, 8, 1),  box (64, 64, 8, 1): the whole q of one sequence
   CUtensorMap ck;   // (64, max_nc, 8, S), box (64, 128, 2, 1)
@@ -390,7 +359,7 @@ struct CombSeq {
 // holds data (an empty split's run was never copied), `seq_a(f)` whether run
 // f belongs to the group's first sequence.  A row of the other sequence reads
 // some in-bounds words and replaces them by zeros with weight 0.
-template <bool kF32, int NK, int NU, typename RunOf, typename SeqA>
+template <int NK, int NU, typename RunOf, typename SeqA>
 __device__ __forceinline__ void merge_runs(const uint8_t* smem, int fs, int fe,
                                            const bool (&rowA)[4], const int (&hrow)[4],
                                            const uint32_t (&roff)[4], const float (&Mu)[4],
@@ -398,8 +367,7 @@ __device__ __forceinline__ void merge_runs(const uint8_t* smem, int fs, int fe,
                                            SeqA&& seq_a) {
 #pragma unroll 1
   for (int f = fs; f < fe; f += NU) {
-    constexpr int NX = kF32 ? 4 : 2;
-    uint4 x[NU][NK][NX];
+    uint4 x[NU][NK][2];
     float w[NU][NK];
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
@@ -412,36 +380,25 @@ __device__ __forceinline__ void merge_runs(const uint8_t* smem, int fs, int fe,
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
         const uint4* row = reinterpret_cast<const uint4*>(smem + kSmemQ + base + roff[k]);
-#pragma unroll
-        for (int q = 0; q < NX; ++q) x[u][k][q] = row[kF32 ? 32 * q : q];
+        x[u][k][0] = row[0];
+        x[u][k][1] = row[1];
         const float mi = ml[hrow[k]], li = ml[64 + hrow[k]];
         // the partial row is normalised: its weight carries its sum l
         const bool mine = live && rowA[k] == inA;
         w[u][k] = (mine && mi != -INFINITY) ? li * ex2_approx(mi - Mu[k]) : 0.f;
         if (!mine) {  // not this row's data (or never copied): may hold anything
-#pragma unroll
-          for (int q = 0; q < NX; ++q) x[u][k][q] = make_uint4(0u, 0u, 0u, 0u);
+          x[u][k][0] = make_uint4(0u, 0u, 0u, 0u);
+          x[u][k][1] = make_uint4(0u, 0u, 0u, 0u);
         }
       }
     }
     // lane l: rows 4l + t (t = 0..3) of the [128][4] layout, i.e. value
-    // columns 128c + 4l + t, in words (t, c = 0|1) and (t, c = 2|3); fp32: the
-    // same columns, four in a row for each c
+    // columns 128c + 4l + t, in words (t, c = 0|1) and (t, c = 2|3)
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
         L[k] += w[u][k];
-        if constexpr (kF32) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            acc[k][4 * q] = fmaf(w[u][k], __uint_as_float(x[u][k][q].x), acc[k][4 * q]);
-            acc[k][4 * q + 1] = fmaf(w[u][k], __uint_as_float(x[u][k][q].y), acc[k][4 * q + 1]);
-            acc[k][4 * q + 2] = fmaf(w[u][k], __uint_as_float(x[u][k][q].z), acc[k][4 * q + 2]);
-            acc[k][4 * q + 3] = fmaf(w[u][k], __uint_as_float(x[u][k][q].w), acc[k][4 * q + 3]);
-          }
-          continue;
-        }
         const uint32_t wd[8] = {x[u][k][0].x, x[u][k][0].y, x[u][k][0].z, x[u][k][0].w,
                                 x[u][k][1].x, x[u][k][1].y, x[u][k][1].z, x[u][k][1].w};
 #pragma unroll
@@ -456,24 +413,20 @@ __device__ __forceinline__ void merge_runs(const uint8_t* smem, int fs, int fe,
   }
 }
 
-// `split`: CTAs the tiles are split over (paged cache: no more than there are
-// tiles, so that no split is empty; `grid` of them merge rows either way).
-template <bool kF32, typename GridArrive, typename GridWait>
+template <typename GridArrive, typename GridWait>
 __device__ __forceinline__ void combine_cta(const Params& p, const long long* tiles, int grid,
-                                            int split,
                                             uint8_t* smem, uint32_t sbase, uint32_t bar_comb,
                                             volatile int* abort_flag, int warp, int lane,
                                             GridArrive&& grid_arrive, GridWait&& grid_wait) {
   const long long N = tiles[p.S];
   // CTA that owns global tile x: ceil((x + 1) * grid / N) - 1
   auto owner = [&](long long x) -> int {
-    return static_cast<int>(div_nn((x + 1) * split + N - 1, N)) - 1;
+    return static_cast<int>(div_nn((x + 1) * grid + N - 1, N)) - 1;
   };
   // With at least one tile per CTA every split is non-empty: the 64-bit
   // divisions of the general test are kept off the common path.
-  constexpr uint32_t kRow = kDim * (kF32 ? 4 : 2);   // bytes of a partial row
-  const bool dense = kF32 || N >= split;
-  auto nonempty = [&](int c) { return dense || div_nn(N * c, split) < div_nn(N * (c + 1), split); };
+  const bool dense = N >= grid;
+  auto nonempty = [&](int c) { return dense || div_nn(N * c, grid) < div_nn(N * (c + 1), grid); };
   auto seq = [&](int s, int h0, int nh) -> CombSeq {
     CombSeq q;
     q.s = s;
@@ -497,8 +450,8 @@ __device__ __forceinline__ void combine_cta(const Params& p, const long long* ti
     const CombSeq A = seq(sA, hA, nA);
     const CombSeq B = (ng > nA) ? seq(sA + 1, 0, ng - nA) : CombSeq{sA + 1, 0, 0, 0, 0};
     const int nItems = A.n + B.n;
-    const uint32_t szA = static_cast<uint32_t>(A.nh) * kRow;
-    const uint32_t szB = static_cast<uint32_t>(B.nh) * kRow;
+    const uint32_t szA = static_cast<uint32_t>(A.nh) * kDim * 2;
+    const uint32_t szB = static_cast<uint32_t>(B.nh) * kDim * 2;
 
     // this warp's rows: merge state and sigmoid(g)
     float M[4], L[4], acc[4][16];
@@ -560,8 +513,7 @@ __device__ __forceinline__ void combine_cta(const Params& p, const long long* ti
           const uint32_t sz = inA ? szA : szB;
           if (nonempty(c)) {
             const size_t slot = static_cast<size_t>(c + q.s);
-            const uint8_t* src = reinterpret_cast<const uint8_t*>(p.ws_o) +
-                                 (slot * kHeads + q.h0) * kRow;
+            const uint16_t* src = p.ws_o + (slot * kHeads + q.h0) * kDim;
             asm volatile(
                 "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes"
                 " [%0], [%1], %2, [%3];" ::"r"(sbase + kSmemQ + off),
@@ -623,7 +575,7 @@ __device__ __forceinline__ void combine_cta(const Params& p, const long long* ti
         rowA[k] = i < A.nh;
         const int r = rowA[k] ? i : i - A.nh;
         hrow[k] = (rowA[k] ? A.h0 : B.h0) + r;
-        roff[k] = static_cast<uint32_t>(r) * kRow + (kF32 ? 16u : 32u) * lane;
+        roff[k] = static_cast<uint32_t>(r) * kDim * 2 + 32u * lane;
       }
       auto run_of = [&](int f, bool& live) -> uint32_t {
         const bool inA = f < A.n;
@@ -635,13 +587,13 @@ __device__ __forceinline__ void combine_cta(const Params& p, const long long* ti
       auto seq_a = [&](int f) { return f < A.n; };
       const int nk = ng > warp ? min(4, (ng - warp + 6) / 7) : 0;
       if (nk == 4)
-        merge_runs<kF32, 4, 1>(smem, fs, fe, rowA, hrow, roff, Mu, L, acc, run_of, seq_a);
+        merge_runs<4, 1>(smem, fs, fe, rowA, hrow, roff, Mu, L, acc, run_of, seq_a);
       else if (nk == 3)
-        merge_runs<kF32, 3, 1>(smem, fs, fe, rowA, hrow, roff, Mu, L, acc, run_of, seq_a);
+        merge_runs<3, 1>(smem, fs, fe, rowA, hrow, roff, Mu, L, acc, run_of, seq_a);
       else if (nk == 2)
-        merge_runs<kF32, 2, 2>(smem, fs, fe, rowA, hrow, roff, Mu, L, acc, run_of, seq_a);
+        merge_runs<2, 2>(smem, fs, fe, rowA, hrow, roff, Mu, L, acc, run_of, seq_a);
       else if (nk == 1)
-        merge_runs<kF32, 1, 4>(smem, fs, fe, rowA, hrow, roff, Mu, L, acc, run_of, seq_a);
+        merge_runs<1, 4>(smem, fs, fe, rowA, hrow, roff, Mu, L, acc, run_of, seq_a);
       __syncthreads();  // the next batch overwrites the buffers
       fs = fe;
     }
@@ -702,9 +654,11 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
 // factors sit in shared memory as fp32, padded with zeros to a multiple of 8
 // ranks.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ int vha_rank8(const Params& p) { return (p.vha_rank + 7) & ~7; }
+template <typename P>
+__device__ __forceinline__ int vha_rank8(const P& p) { return (p.vha_rank + 7) & ~7; }
 
-__device__ __forceinline__ void vha_load_factors(const Params& p, float* fd, float* fu) {
+template <int kThreads, typename P>
+__device__ __forceinline__ void vha_load_factors(const P& p, float* fd, float* fu) {
   const int r = p.vha_rank, r8 = vha_rank8(p);
   for (int i = threadIdx.x; i < kHeads * r8; i += kThreads) {
     const int h = i / r8, rr = i - h * r8;
@@ -714,7 +668,8 @@ __device__ __forceinline__ void vha_load_factors(const Params& p, float* fd, flo
   }
 }
 
-__device__ __forceinline__ void vha_mix_columns(const Params& p, const float* fd, const float* fu,
+template <int kThreads, typename P>
+__device__ __forceinline__ void vha_mix_columns(const P& p, const float* fd, const float* fu,
                                                 uint16_t* tile, int warp, int lane) {
   const int r8 = vha_rank8(p);
   const int wpc = kThreads / 32;
@@ -785,32 +740,9 @@ __device__ __forceinline__ void vha_mix_columns(const Params& p, const float* fd
   }
 }
 
-// Page number of box `b` of the 128-entry tile `j` for the producer lane that
-// loads it: num_pages (zero fill) for a box past the last visible entry or a
-// page number outside the pool (reported).
-__device__ __forceinline__ int box_page(const Params& p, const int* row, int nc, int j, int b) {
-  const int e = j * kKeyTile + (b << min(p.page_shift, 7));
-  if (e >= nc) return p.num_pages;
-  const int pg = __ldg(row + (e >> p.page_shift));
-  if (static_cast<unsigned>(pg) < static_cast<unsigned>(p.num_pages)) return pg;
-  record_error(DEVERR_BAD_INPUT, 102);
-  return p.num_pages;
-}
-
-// Keys of the last stage rows that P.V reads: [valid, 16-aligned end) of a
-// [128 keys][64] x 2 slab stage are cleared by the calling warp.
-__device__ __forceinline__ void clear_rows(uint8_t* stage, int valid, int lane) {
-  const int end = (valid + 15) & ~15;
-  for (int i = valid * 8 + lane; i < end * 8; i += 32) {
-    *reinterpret_cast<uint4*>(stage + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-    *reinterpret_cast<uint4*>(stage + kSlab + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-  }
-}
-
-template <bool kF8, bool kPaged>
+template <bool kF8>
 __global__ void __launch_bounds__(kThreads, 1)
-    decode_kernel(const __grid_constant__ Maps maps, const Params p0) {
-  Params p = p0;
+    decode_kernel(const __grid_constant__ Maps maps, const Params p) {
   constexpr int NS = kF8 ? kStagesF8 : kStages;   // ring stages
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte aligned, derived from smem_raw itself so that the compiler
@@ -867,17 +799,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // sequences, else by the plan kernel, which may still be running
   // (programmatic dependent launch): wait for it.  Either way a CTA barrier
   // follows, which also publishes the set-up above.
-  const bool inl = p0.S <= kInlineSeqs;   // as the launch decided
+  const bool inl = p.S <= kInlineSeqs;
   long long* sT = reinterpret_cast<long long*>(smem + kSmemTiles);
   int* sL = reinterpret_cast<int*>(smem + kSmemCtx);
-  if constexpr (kPaged) {
-    // launched while the append (or the plan) may still run: what follows reads its results
-    if (inl && p.plan_early) inline_plan(p, sT, sL);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (p.count != nullptr) p.S = min(max(*p.count, 0), p0.S);
-  }
   if (inl) {
-    if (!kPaged || !p.plan_early) inline_plan(p, sT, sL);
+    inline_plan(p, sT, sL);
   } else {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __syncthreads();
@@ -887,14 +813,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long* tiles = inl ? sT : p.seq_tile;
   const int* lens = inl ? sL : p.ctx_len;
   const long long N = tiles[p.S];
-  // CTAs the tiles are split over: with fewer tiles than CTAs one tile each, so
-  // that merging never looks at splits without a tile (81 us instead of a few
-  // for one short sequence)
-  const int split = kPaged ? static_cast<int>(min(static_cast<long long>(gridDim.x), max(N, 1LL)))
-                           : static_cast<int>(gridDim.x);
-  const bool splits = !kPaged || static_cast<int>(blockIdx.x) < split;
-  const long long A0 = splits ? div_nn(N * blockIdx.x, split) : 0;
-  const long long A1 = splits ? div_nn(N * (blockIdx.x + 1), split) : 0;
+  const long long A0 = div_nn(N * blockIdx.x, gridDim.x);
+  const long long A1 = div_nn(N * (blockIdx.x + 1), gridDim.x);
   if (A0 < A1) {  // uniform across the CTA; a CTA without tiles only helps combine
 
   // Segments: maximal runs of this CTA's tiles inside one sequence.
@@ -949,21 +869,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       --npend;
       return true;
     };
-    // code tile (channels [64 z, 64 z + 128), rows y..y+127) of use u; paged
-    // entries (boxes > 0): lane b loads the box of page `w`, its own
-    auto load = [&](const CUtensorMap* map, int y, int z, int w, int boxes = 0) -> bool {
+    // code tile (channels [64 z, 64 z + 128), rows y..y+127) of use u
+    auto load = [&](const CUtensorMap* map, int y, int z, int w) -> bool {
       if ((u & 1) == static_cast<uint32_t>(me)) {
         if (npend == 2 && !convert_oldest()) return false;
         const uint32_t slot = nown & 1;
-        const uint32_t dst = sStg + (2 * me + slot) * kStgBytes;
-        if (lane == 0) mbar_expect_tx(bar(B_STG + 2 * me + slot), kStgBytes);
-        if (kPaged && boxes > 0) {
-          __syncwarp();
-          if (lane < boxes)
-            tma_load_3d(dst + lane * (kStgBytes / boxes), map, bar(B_STG + 2 * me + slot), 64 * z,
-                        0, w);
-        } else if (lane == 0) {
-          tma_load_3d(dst, map, bar(B_STG + 2 * me + slot), 64 * z, y, w);
+        if (lane == 0) {
+          mbar_expect_tx(bar(B_STG + 2 * me + slot), kStgBytes);
+          tma_load_3d(sStg + (2 * me + slot) * kStgBytes, map, bar(B_STG + 2 * me + slot), 64 * z,
+                      y, w);
         }
         ++nown;
         ++npend;
@@ -989,19 +903,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
       ++quse;
-      const int boxes = kPaged ? kKeyTile >> min(p.page_shift, 7) : 0;
-      const int* prow = kPaged ? p.table + s * p.table_ld : nullptr;
-      auto load_tile = [&](const CUtensorMap* comp, const CUtensorMap* win, int j) -> bool {
-        int w = s;
-        if constexpr (kPaged) {
-          if (j < si.nct) w = box_page(p, prow, si.nc, j, lane & (boxes - 1));
-        }
+      auto load_k = [&](int j) -> bool {
         for (int d = 0; d < 4 && ok; ++d)
-          ok = (j < si.nct) ? load(comp, j * kKeyTile, 2 * d, w, boxes) : load(win, 0, 2 * d, s);
+          ok = (j < si.nct) ? load(&maps.ck, j * kKeyTile, 2 * d, s) : load(&maps.wk, 0, 2 * d, s);
         return ok;
       };
-      auto load_k = [&](int j) -> bool { return load_tile(&maps.ck, &maps.wk, j); };
-      auto load_v = [&](int j) -> bool { return load_tile(&maps.cv, &maps.wv, j); };
+      auto load_v = [&](int j) -> bool {
+        for (int e = 0; e < 4 && ok; ++e)
+          ok = (j < si.nct) ? load(&maps.cv, j * kKeyTile, 2 * e, s) : load(&maps.wv, 0, 2 * e, s);
+        return ok;
+      };
       if (!load_k(j0)) break;
       for (int j = j0; j < j1 && ok; ++j) {
         if (j + 1 < j1 && !load_k(j + 1)) break;
@@ -1011,76 +922,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     while (ok && npend > 0) ok = convert_oldest();
     if (me == 0 && lane == 0) {
-      const long long R = static_cast<long long>(p.S) * kHeads;
-      const long long r0 = div_nn(R * blockIdx.x, gridDim.x);
-      const long long r1 = div_nn(R * (blockIdx.x + 1), gridDim.x);
-      if (r1 > r0)
-        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.g + r0 * kDim),
-                     "r"(static_cast<uint32_t>(r1 - r0) * kDim * 2)
-                     : "memory");
-    }
-  } else if (warp <= 1 && kPaged) {
-    // ------------------------------------------------------------ producers, paged bf16 cache
-    // As below, with the boxes of a stage issued by one lane each.
-    const int me = warp;
-    const int boxes = kKeyTile >> min(p.page_shift, 7);       // per slab: 1, 2, 4 or 8
-    const int bx = lane & (boxes - 1), slab = lane / boxes;
-    const uint32_t boff = slab * kSlab + bx * (kSlab / boxes);
-    uint32_t u = 0, quse = 0;
-    bool ok = true;
-    // stage of the slabs 2 d, 2 d + 1: entries of the page `pg` of this lane's box, or
-    // (pg < 0) the window rows from y on
-    auto load = [&](const CUtensorMap* map, int d, int pg, int y) {
-      if ((u & 1) == static_cast<uint32_t>(me)) {
-        const uint32_t st = u % NS;
-        if (lane == 0) {
-          ok = mbar_wait(bar(B_EMPTY + st), ((u / NS) & 1) ^ 1, abort_flag, kWaitLimitNs, 40);
-          if (ok) mbar_expect_tx(bar(B_FULL + st), kStage);
-        }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        __syncwarp();
-        if (ok && pg >= 0 && slab < 2)
-          tma_load_4d_dec(sRing + st * kStage + boff, map, bar(B_FULL + st), 0, 0, 2 * d + slab, pg);
-        else if (ok && pg < 0 && lane == 0)
-          tma_load_4d_dec(sRing + st * kStage, map, bar(B_FULL + st), 0, y, 2 * d, 0);
-      }
-      ++u;
-    };
-    long long x = A0;
-    for (int s = s_first; x < A1 && ok; ++s) {
-      const SeqInfo si = seq_info(lens, p.max_nc, s);
-      const long long seg_end = min(A1, tiles[s + 1]);
-      const int j0 = static_cast<int>(x - tiles[s]);
-      const int j1 = static_cast<int>(seg_end - tiles[s]);
-      const int* prow = p.table + (p.row_of != nullptr ? p.row_of[s] : s) * p.table_ld;
-      const int win = p.win_row != nullptr ? p.win_row[s] : s * kWin;
-      auto page_of = [&](int j) -> int {
-        return j < si.nct ? box_page(p, prow, si.nc, j, bx) : -1;
-      };
-      int pg = page_of(j0), pg1 = j0 + 1 < j1 ? page_of(j0 + 1) : -1;
-      if (me == 0) {
-        if (lane == 0) {
-          ok = mbar_wait(bar(B_QEMPTY), (quse & 1) ^ 1, abort_flag, kWaitLimitNs, 41);
-          if (ok) {
-            mbar_expect_tx(bar(B_QFULL), 8 * kQSlab);
-            tma_load_4d_dec(sQ, &maps.q, bar(B_QFULL), 0, s * kHeads, 0, 0);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      }
-      ++quse;
-      for (int d = 0; d < 4 && ok; ++d) load(pg >= 0 ? &maps.ck : &maps.wk, d, pg, win);
-      for (int j = j0; j < j1 && ok; ++j) {
-        const int pg2 = j + 2 < j1 ? page_of(j + 2) : -1;   // needed one tile later
-        if (j + 1 < j1)
-          for (int d = 0; d < 4 && ok; ++d) load(pg1 >= 0 ? &maps.ck : &maps.wk, d, pg1, win);
-        for (int d = 0; d < 4 && ok; ++d) load(pg >= 0 ? &maps.cv : &maps.wv, d, pg, win);
-        pg = pg1;
-        pg1 = pg2;
-      }
-      x = seg_end;
-    }
-    if (me == 0 && lane == 0) {   // the gate rows this CTA combines
       const long long R = static_cast<long long>(p.S) * kHeads;
       const long long r0 = div_nn(R * blockIdx.x, gridDim.x);
       const long long r1 = div_nn(R * (blockIdx.x + 1), gridDim.x);
@@ -1150,106 +991,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                        : "memory");
       }
     }
-  } else if (warp == 2 && kPaged && !kF8) {
-    // ------------------------------------------------------------ MMA issuer, paged bf16 cache
-    // Lane 0 waits and issues; the whole warp walks the tiles, to clear the
-    // V rows behind the last visible key of a tile that is not full.  Only
-    // lane 0 knows of a failed wait (`ok`), so nobody leaves the loops early.
-    const bool lead = lane == 0;
-    bool ok = true;
-    uint32_t ring = 0, quse = 0, sidx = 0, pvidx = 0, nseg = 0;
-    const uint32_t idesc_s = idesc_bf16_f32(128, 64, false, false);
-    const uint32_t idesc_o = idesc_bf16_f32(128, 64, true, true);
-    auto issue_s = [&]() {
-      if (lead && ok) {
-        const uint32_t buf = sidx & 1;
-        ok = mbar_wait(bar(B_SFREE + buf), ((sidx >> 1) & 1) ^ 1, abort_flag, kWaitLimitNs, 50);
-        tc_fence_after();
-        const uint32_t dS = tmem + (buf ? kTmemS1 : kTmemS0);
-        for (int d2 = 0; d2 < 4 && ok; ++d2) {
-          const uint32_t st = (ring + d2) % NS;
-          ok = mbar_wait(bar(B_FULL + st), ((ring + d2) / NS) & 1, abort_flag, kWaitLimitNs, 51);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int sl = 0; sl < 2; ++sl) {
-            const int d = 2 * d2 + sl;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_bf16(dS, sdesc_sw128(sRing + st * kStage + sl * kSlab + 32 * k, 16, 1024),
-                        sdesc_sw128(sQ + d * kQSlab + 32 * k, 16, 1024), idesc_s, (d | k) != 0);
-          }
-          umma_commit(bar(B_EMPTY + st));
-        }
-        if (ok) umma_commit(bar(B_SFULL + buf));
-      }
-      ring += 4;
-      ++sidx;
-    };
-    auto issue_pv = [&](bool first, int valid) {
-      if (lead && ok) {
-        ok = mbar_wait(bar(B_PFULL), pvidx & 1, abort_flag, kWaitLimitNs, 52);
-        if (ok && first)
-          ok = mbar_wait(bar(B_OFREE), (nseg & 1) ^ 1, abort_flag, kWaitLimitNs, 53);
-        tc_fence_after();
-      }
-      const int ksteps = (valid + 15) >> 4;
-      for (int c = 0; c < 4; ++c, ++ring) {
-        const uint32_t st = ring % NS, par = (ring / NS) & 1;
-        if (lead && ok) ok = mbar_wait(bar(B_FULL + st), par, abort_flag, kWaitLimitNs, 54);
-        if ((valid & 15) != 0) {
-          if (__shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0) {
-            mbar_try_wait(bar(B_FULL + st), par);   // this lane's acquire
-            clear_rows(smem + kSmemRing + st * kStage, valid, lane);
-            fence_proxy_async_smem();               // read next by the tensor core
-          }
-          __syncwarp();
-        }
-        if (lead && ok) {
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k < ksteps)
-              umma_bf16(tmem + kTmemO + 64 * c,
-                        sdesc_sw128(sRing + st * kStage + 2048 * k, kSlab, 1024),
-                        sdesc_sw128(sPT + 2048 * k, kSlab, 1024), idesc_o,
-                        (!first || k > 0) ? 1u : 0u);
-          umma_commit(bar(B_EMPTY + st));
-        }
-      }
-      if (lead && ok) umma_commit(bar(B_PFREE));
-      ++pvidx;
-    };
-    long long x = A0;
-    for (int s = s_first; x < A1; ++s) {
-      const SeqInfo si = seq_info(lens, p.max_nc, s);
-      const long long seg_end = min(A1, tiles[s + 1]);
-      const int j0 = static_cast<int>(x - tiles[s]);
-      const int j1 = static_cast<int>(seg_end - tiles[s]);
-      if (lead && ok) {
-        ok = mbar_wait(bar(B_QFULL), quse & 1, abort_flag, kWaitLimitNs, 56);
-        tc_fence_after();
-      }
-      ++quse;
-      issue_s();
-      if (lead && ok && j1 - j0 == 1) umma_commit(bar(B_QEMPTY));
-      for (int j = j0; j < j1; ++j) {
-        if (j + 1 < j1) {
-          issue_s();
-          if (lead && ok && j + 2 == j1) umma_commit(bar(B_QEMPTY));
-        }
-        issue_pv(j == j0, j < si.nct ? min(kKeyTile, si.nc - j * kKeyTile)
-                          : p.win_row != nullptr ? kWin : min(si.L, kWin));
-      }
-      if (lead && ok) umma_commit(bar(B_OFULL));
-      ++nseg;
-      x = seg_end;
-    }
-    if (lead) {
-      umma_commit(bar(B_DRAIN));
-      mbar_wait(bar(B_DRAIN), 0, abort_flag, kWaitLimitNs, 57);
-    }
-    __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
@@ -1386,14 +1127,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool comp = j < si.nct;
           const int e = j * kKeyTile + key;
           if (comp ? e < si.nc : ((si.L >= kWin) || (key < si.L))) {
-            size_t ix = comp ? static_cast<size_t>(s) * p.max_nc + e
-                             : static_cast<size_t>(s) * kWin + key;
-            if (kPaged && comp) {   // a page outside the pool: zero codes, any scale
-              const int pg = __ldg(p.table + s * p.table_ld + (e >> p.page_shift));
-              ix = static_cast<unsigned>(pg) < static_cast<unsigned>(p.num_pages)
-                       ? (static_cast<size_t>(pg) << p.page_shift) + (e & ((1 << p.page_shift) - 1))
-                       : 0;
-            }
+            const size_t ix = comp ? static_cast<size_t>(s) * p.max_nc + e
+                                   : static_cast<size_t>(s) * kWin + key;
             sk = __ldg((comp ? p.sck : p.swk) + ix);
             sv = __ldg((comp ? p.scv : p.swv) + ix);
           }
@@ -1413,7 +1148,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // validity of this thread's key
         bool valid;
         if (j < si.nct) valid = j * kKeyTile + key < si.nc;
-        else if (kPaged && p.win_row != nullptr) valid = key >= kWin - si.L;   // positions >= 0
         else valid = (si.L >= kWin) || (key < si.L);
         float a[64];
         const float sc = p.scale_log2 * sk;
@@ -1511,7 +1245,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_bar_sync(1, 128);
       const int slot = blockIdx.x + s;
       uint2* wo = reinterpret_cast<uint2*>(p.ws_o + static_cast<size_t>(slot) * kHeads * kDim) + key;
-      float* wf = reinterpret_cast<float*>(p.ws_o) + static_cast<size_t>(slot) * kHeads * kDim + key;
 #pragma unroll 1
       for (int hh = 0; hh < 64; hh += 16) {
         uint32_t o[64];
@@ -1522,12 +1255,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const float inv = red[R_ALPHA + hh + i];
-          if constexpr (kPaged) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              wf[(hh + i) * kDim + 128 * c] = __uint_as_float(o[16 * c + i]) * inv;
-            continue;
-          }
           wo[(hh + i) * kKeyTile] =
               make_uint2(pack_bf16x2(__uint_as_float(o[i]) * inv, __uint_as_float(o[16 + i]) * inv),
                          pack_bf16x2(__uint_as_float(o[32 + i]) * inv,
@@ -1604,8 +1331,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) fence_proxy_async_all();
     __syncthreads();
   };
-  combine_cta<kPaged>(p, tiles, gridDim.x, split, smem, sbase, bar(B_COMB), abort_flag, warp, lane,
-                      grid_arrive, grid_wait);
+  combine_cta(p, tiles, gridDim.x, smem, sbase, bar(B_COMB), abort_flag, warp, lane,
+              grid_arrive, grid_wait);
   if (!kF8 && p.vha_rank > 0) {
     // the combine's buffers are free once every warp is here
     float* fd = reinterpret_cast<float*>(smem + kSmemQ);   // [64][r8]
@@ -1613,10 +1340,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint16_t* tiles = reinterpret_cast<uint16_t*>(fu + kHeads * kHeads);   // 1 KB per warp
     __syncthreads();
     grid_wait();    // the first barrier is complete (a no-op if combining waited for it)
-    vha_load_factors(p, fd, fu);
+    vha_load_factors<kThreads>(p, fd, fu);
     grid_arrive();  // this CTA's rows of out are written (second barrier of the launch)
     grid_wait();
-    vha_mix_columns(p, fd, fu, tiles + warp * kHeads * 8, warp, lane);
+    vha_mix_columns<kThreads>(p, fd, fu, tiles + warp * kHeads * 8, warp, lane);
   }
 }
 

@@ -22,6 +22,7 @@
 #include "backward.cuh"
 #include "quant.cuh"
 #include "paged.cuh"
+#include "paged_decode.cuh"
 #include "pages.cuh"
 
 namespace {
@@ -97,15 +98,14 @@ bool make_map_bytes(CUtensorMap* m, const void* base, uint64_t rows, uint32_t bo
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 3-D byte view [Z][Y][512] of e4m3 code rows, box (128 bytes, box_rows, 1),
-// no swizzle: one 128-channel code tile (128 keys, or one page of fewer).
-bool make_map_codes(CUtensorMap* m, const void* base, uint64_t Y, uint64_t Z,
-                    uint32_t box_rows = 128) {
+// 3-D byte view [Z][Y][512] of e4m3 code rows, box (128 bytes, 128 rows, 1),
+// no swizzle: one 128-channel, 128-key code tile.
+bool make_map_codes(CUtensorMap* m, const void* base, uint64_t Y, uint64_t Z) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return false;
   const cuuint64_t dims[3] = {512, Y, Z};
   const cuuint64_t strides[2] = {512, 512 * Y};
-  const cuuint32_t box[3] = {128, box_rows, 1};
+  const cuuint32_t box[3] = {128, 128, 1};
   const cuuint32_t es[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
@@ -171,18 +171,18 @@ cudaError_t once_per_device(F&& f) {
 // (the decode kernel then starts early and waits for it inside), else the
 // decode kernel alone, which plans for itself.  Cooperative either way: the
 // kernel holds a grid barrier.
-template <bool kF8, bool kPaged = false>
+template <bool kF8>
 cudaError_t launch_decode(const hca::decode::Maps& maps, const hca::decode::Params& prm, int grid,
                           cudaStream_t stream) {
   namespace D = hca::decode;
-  cudaError_t err = once_per_device<kF8 ? (kPaged ? 3 : 2) : (kPaged ? 1 : 0)>([] {
-    return cudaFuncSetAttribute(D::decode_kernel<kF8, kPaged>,
+  cudaError_t err = once_per_device<kF8 ? 1 : 0>([] {
+    return cudaFuncSetAttribute(D::decode_kernel<kF8>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, D::kSmemAlloc);
   });
   if (err != cudaSuccess) return err;
   const bool inl = prm.S <= D::kInlineSeqs;
   if (!inl) {
-    D::plan_kernel<<<1, 1024, 0, stream>>>(prm.ctx_len, prm.S, prm.max_nc, prm.seq_tile, prm.count);
+    D::plan_kernel<<<1, 1024, 0, stream>>>(prm.ctx_len, prm.S, prm.max_nc, prm.seq_tile);
     err = cudaGetLastError();
     if (err != cudaSuccess) return err;
   }
@@ -197,8 +197,8 @@ cudaError_t launch_decode(const hca::decode::Maps& maps, const hca::decode::Para
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = inl && !kPaged ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, D::decode_kernel<kF8, kPaged>, maps, prm);
+  cfg.numAttrs = inl ? 1 : 2;
+  return cudaLaunchKernelEx(&cfg, D::decode_kernel<kF8>, maps, prm);
 }
 
 hca_status_t launch_status() {

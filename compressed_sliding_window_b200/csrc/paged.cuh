@@ -214,7 +214,8 @@ struct Queries {
   int* len;        // [N] context length of the query
   int* row_of;     // [N] its page table row
   int* win_row;    // [N] its first window row
-  unsigned long long* gsync;   // the attention's grid barrier, reset here
+  unsigned long long* gsync;   // the attention's grid barrier and
+  unsigned* arrived;           // [N] counters, reset here
   // four positions at a time
   int4* items;     // [cap] {table row, first packed token, its position, positions}
   int cap;
@@ -250,6 +251,7 @@ __global__ void __launch_bounds__(kFinishThreads)
       qr.len[sp.qs + r] = sp.L0 + r + 1;
       qr.row_of[sp.qs + r] = i;
       qr.win_row[sp.qs + r] = base + r;
+      qr.arrived[sp.qs + r] = 0u;
     }
     if (i == 0 && blockIdx.y == 0 && tid == 0) {
       *qr.count = min(max(c.q_start[c.S], 0), c.N);

@@ -80,20 +80,22 @@ long long entry_units(int S, int N) {
   return N / hca::paged::kBlk + static_cast<long long>(hca::paged::kUnitsExtra) * S;
 }
 
-// Decode parameters over a paged cache; `rows`: queries (and their maps' rows).
+// One query at a time, split over the keys: the rest of `prm`, maps, launches.
 hca_status_t paged_attend(const hca::paged::Cache& c, const hca_bf16* q, const hca_bf16* g,
                           hca_bf16* out, const hca_bf16* wk, const hca_bf16* wv,
-                          uint64_t win_rows, hca::decode::Params& prm, uint8_t* ws,
+                          uint64_t win_rows, hca::pdecode::Params& prm, uint8_t* ws,
                           cudaStream_t stream) {
-  namespace D = hca::decode;
+  namespace D = hca::pdecode;
   const int sms = device_sms();
   if (sms <= 0) return HCA_ERR_CUDA;
   const int slots = sms + prm.S;
-  prm.max_nc = c.max_pages << c.page_shift;
+  prm.max_nc = c.num_pages > 0 ? c.max_pages << c.page_shift : 0;
   prm.gsync = reinterpret_cast<unsigned long long*>(ws);
-  prm.ws_o = reinterpret_cast<uint16_t*>(ws + 256);
-  prm.ws_ml = reinterpret_cast<float*>(ws + 256 + D::ws_o_bytes(slots, true));
-  prm.seq_tile = reinterpret_cast<long long*>(ws + 256 + align256(D::ws_bytes(slots, true)));
+  prm.arrived = reinterpret_cast<unsigned*>(ws + 256);
+  ws += 256 + align256(static_cast<size_t>(prm.S) * 4);
+  prm.ws_o = reinterpret_cast<float*>(ws);
+  prm.ws_ml = reinterpret_cast<float*>(ws + D::ws_o_bytes(slots));
+  prm.seq_tile = reinterpret_cast<long long*>(ws + align256(D::ws_bytes(slots)));
   prm.g = g;
   prm.out = out;
   prm.table = c.table;
@@ -108,14 +110,35 @@ hca_status_t paged_attend(const hca::paged::Cache& c, const hca_bf16* q, const h
   if (ok && c.num_pages > 0) {
     ok = make_map4(&maps.ck, c.ck, box, c.num_pages, box, 1) &&
          make_map4(&maps.cv, c.cv, box, c.num_pages, box, 1);
-  } else if (ok) {   // no page exists: every box falls outside of these
-    prm.num_pages = 0;
-    prm.max_nc = 0;
+  } else if (ok) {   // no entry can be visible: never used
     maps.ck = maps.wk;
     maps.cv = maps.wv;
   }
   if (!ok) return HCA_ERR_CUDA;
-  if (launch_decode<false, true>(maps, prm, sms, stream) != cudaSuccess) return HCA_ERR_CUDA;
+  if (once_per_device<2>([] {
+        return cudaFuncSetAttribute(D::paged_decode_kernel,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, D::kSmemAlloc);
+      }) != cudaSuccess)
+    return HCA_ERR_CUDA;
+  if (prm.S > D::kInlineSeqs) {
+    D::plan_kernel<<<1, 1024, 0, stream>>>(prm.ctx_len, prm.S, prm.max_nc, prm.seq_tile, prm.count);
+    if (cudaGetLastError() != cudaSuccess) return HCA_ERR_CUDA;
+  }
+  // cooperative: CTAs that share a query wait for one another
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sms);
+  cfg.blockDim = dim3(D::kThreads);
+  cfg.dynamicSmemBytes = D::kSmemAlloc;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, D::paged_decode_kernel, maps, prm) != cudaSuccess)
+    return HCA_ERR_CUDA;
   return launch_status();
 }
 
@@ -320,6 +343,7 @@ hca_status_t hca_paged_prefill(const hca_bf16* q, const hca_bf16* g, const hca_b
     qr.row_of = reinterpret_cast<int*>(w + L.row_of);
     qr.win_row = reinterpret_cast<int*>(w + L.win_row);
     qr.gsync = reinterpret_cast<unsigned long long*>(w + L.decode);
+    qr.arrived = reinterpret_cast<unsigned*>(w + L.decode + 256);
   } else {
     qr.items = reinterpret_cast<int4*>(w + L.list);
     qr.cap = L.items;
@@ -334,7 +358,7 @@ hca_status_t hca_paged_prefill(const hca_bf16* q, const hca_bf16* g, const hca_b
   if (!L.split)
     return paged_items(c, L, w, q, g, out, S, N, scale, vha_down, vha_up, vha_rank,
                        paged_clusters(L.items), stream);
-  hca::decode::Params prm = {};
+  hca::pdecode::Params prm = {};
   prm.ctx_len = qr.len;
   prm.S = N;
   prm.scale_log2 = scale * 1.4426950408889634f;
@@ -353,8 +377,8 @@ size_t hca_paged_decode_workspace_size(int S) {
   if (S < 1) return 0;
   const int sms = device_sms();
   if (sms <= 0) return 0;
-  // grid barrier counter, split partials, tile prefix
-  return 256 + align256(hca::decode::ws_bytes(sms + S, true)) + static_cast<size_t>(S + 1) * 8;
+  // grid barrier, counters of the queries, split partials, tile prefix
+  return 256 + align256(static_cast<size_t>(S) * 4) + align256(hca::pdecode::ws_bytes(sms + S)) + static_cast<size_t>(S + 2) * 8;
 }
 
 }  // extern "C"
@@ -373,7 +397,7 @@ hca_status_t paged_decode(const hca_bf16* q, const hca_bf16* g, const int32_t* c
   st = paged_cache(c, cache, S, false);
   if (st != HCA_OK) return st;
   if (ws_bytes < hca_paged_decode_workspace_size(S)) return HCA_ERR_INVALID_ARG;
-  hca::decode::Params prm = {};
+  hca::pdecode::Params prm = {};
   prm.ctx_len = ctx_len;
   prm.S = S;
   prm.scale_log2 = scale * 1.4426950408889634f;
