@@ -570,9 +570,10 @@ def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, s_new: torch.Tensor,
 
 
 def paged_prefill_workspace(S: int, N: int, device) -> torch.Tensor:
-    """Scratch for paged_prefill of N new tokens of S sequences (reusable across calls)."""
+    """A zero-filled workspace for paged_prefill of up to N new tokens of up to S sequences
+    (reusable across calls)."""
     device = _cuda(device)
-    return torch.empty((_sized(device, "hca_paged_prefill_workspace_size", S, N),),
+    return torch.zeros((_sized(device, "hca_paged_prefill_workspace_size", S, N),),
                        dtype=torch.uint8, device=device)
 
 

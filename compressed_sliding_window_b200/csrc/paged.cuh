@@ -210,18 +210,12 @@ constexpr int kFinishThreads = 256;
 
 // What the attention reads beside the cache (null pointers: not wanted).
 struct Queries {
-  // one query at a time (split over the keys)
-  int* len;        // [N] context length of the query
-  int* row_of;     // [N] its page table row
-  int* win_row;    // [N] its first window row
-  unsigned long long* gsync;   // the attention's grid barrier and
-  unsigned* arrived;           // [N] counters, reset here
-  // four positions at a time
+  // four positions at a time; one at a time needs nothing
   int4* items;     // [cap] {table row, first packed token, its position, positions}
   int cap;
   int* tail16;     // [S] first entry of the last group of 16 when it is not full, or INT_MAX
   uint16_t* tail;  // [S, 16, 512] V rows of that group, zeros behind the last entry
-  int* count;      // queries or items in all
+  int* count;      // items in all
 };
 
 // Sum over the CTA (kFinishThreads threads).
@@ -245,19 +239,6 @@ __global__ void __launch_bounds__(kFinishThreads)
   const Span sp = span_of(c, i, blockIdx.y == 0 && tid == 0);
   // launched while entries_kernel may still read the rings
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (qr.len != nullptr) {
-    const int base = raw_base(sp, i);
-    for (int r = blockIdx.y * kFinishThreads + tid; r < sp.n; r += kFinishY * kFinishThreads) {
-      qr.len[sp.qs + r] = sp.L0 + r + 1;
-      qr.row_of[sp.qs + r] = i;
-      qr.win_row[sp.qs + r] = base + r;
-      qr.arrived[sp.qs + r] = 0u;
-    }
-    if (i == 0 && blockIdx.y == 0 && tid == 0) {
-      *qr.count = min(max(c.q_start[c.S], 0), c.N);
-      *qr.gsync = 0ull;
-    }
-  }
   if (qr.items != nullptr) {
     __shared__ long long red[8];
     if (blockIdx.y == 0) {

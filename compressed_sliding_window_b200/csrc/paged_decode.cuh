@@ -29,16 +29,17 @@
 // (The cross-lane form of decode.cuh, 124 shuffles a tile in four warps, takes
 // 4.8 us a tile of 128 keys from L2.)
 //
-// Work split.  The key tiles of all queries laid end to end are cut into one
-// contiguous range per CTA; a query that is whole inside one CTA is written
-// straight out, the others leave partial results (O / l in fp32, m, l), which
-// the CTAs that share the query merge.  When giving each CTA whole queries costs
-// at most kWholeTiles tiles more than an even cut, that is done, and nothing is
-// merged (which takes about as long).
+// Work split.  A query that is whole inside one CTA is written straight out; one
+// that several CTAs share leaves partial results (O / l in fp32, m, l), which
+// they merge.  When giving each CTA whole queries costs at most kWholeTiles
+// tiles more than an even cut, that is done, and nothing is merged (which takes
+// about as long).  Else, with fewer queries than CTAs, each CTA has a part of one
+// query; else the key tiles of all queries laid end to end are cut evenly.
 #pragma once
 
 #include "decode.cuh"
 #include "hca_ptx.cuh"
+#include "paged.cuh"
 
 namespace hca {
 namespace pdecode {
@@ -70,7 +71,8 @@ constexpr int kSmemFlag = kSmemSum + 2 * 4 * 32 * 4;        // [2 parities][2 ha
 constexpr int kSmemBar = kSmemFlag + 64;
 constexpr int kSmemTiles = kSmemBar + 320;                  // [kInlineSeqs + 1] int64 prefix
 constexpr int kSmemLen = kSmemTiles + 8 * (kInlineSeqs + 1) + 8;
-constexpr int kSmemBytes = kSmemLen + 4 * kInlineSeqs;
+constexpr int kSmemRow = kSmemLen + 4 * kInlineSeqs;        // [kInlineSeqs] table row
+constexpr int kSmemBytes = kSmemRow + 4 * kInlineSeqs;
 constexpr int kSmemAlloc = kSmemBytes + 1024;
 static_assert(kSmemAlloc <= 232448 - 1024, "shared memory budget");
 static_assert(kStages * kStage == kKeyTile * kDim * 2, "a tile's K or V is one round of the ring");
@@ -86,8 +88,9 @@ static_assert(kAbortSlot + 4 <= 320, "barrier region overflow");
 
 constexpr uint32_t kTmemO = 0, kTmemS0 = 256, kTmemS1 = 320, kTmemCols = 512;
 
-// Workspace (bytes): [slots][64][512] fp32 partial O / l, then [slots][2][64]
-// fp32 (m, l) in log2 units; slots = grid + S.
+// Workspace (bytes): partial O / l in fp32, [slots][64 chunks][16 heads][32
+// value columns], chunk 16 (head / 16) + column / 32; then [slots][2][64] fp32
+// (m, l) in log2 units; slots = grid + S.
 __host__ __device__ inline size_t ws_o_bytes(int slots) {
   return static_cast<size_t>(slots) * kHeads * kDim * 4;
 }
@@ -103,7 +106,8 @@ struct Params {
   float* ws_o;
   float* ws_ml;
   long long* seq_tile; // [S + 2] tile prefix and longest query (plan_kernel, S > kInlineSeqs)
-  unsigned* arrived;   // [S] arrivals at each query's merge: zero between calls
+  unsigned* arrived;   // [grid] arrivals at the merge of the query whose first CTA is c: zero
+                       // between calls
   unsigned long long* gsync;   // grid barrier of the head mix
   const uint16_t* g;   // [S, 64, 512]
   uint16_t* out;
@@ -114,14 +118,21 @@ struct Params {
   long long table_ld;
   int num_pages;
   int page_shift;
-  const int* row_of;   // [S] table row of each query, null: query s has row s
-  const int* win_row;  // [S] first window row (positions L-128 .. L-1), null: a ring at 128 s
-  const int* count;    // number of queries on the device (at most S), null: S
-  int plan_early;      // ctx_len is older than the kernel in front: plan before waiting for it
+  // Queries that are the tokens of a chunk (chunk.q_start set; S: at most as many):
+  // query i of sequence j has the window rows i + kPad j .. of the laid out raw
+  // tokens.  Else query i is sequence i, its window the ring at row 128 i.
+  paged::Chunk chunk;
+  // The kernel in front writes nothing that is read here but the window rows: only
+  // the loads of those wait for it.  (An entry that it completes is not visible yet:
+  // a block is seen 128 positions after its last token, and a chunk in this form has
+  // fewer.)
+  int only_window;
 };
 
 struct Maps {
   CUtensorMap q;    // (64, S*64, 8, 1),  box (64, 64, 8, 1): the whole q of one query
+  CUtensorMap g;    // (64, S*64, 8, 1),  box (64, 64, 4, 1): half of one query's gate
+  CUtensorMap out;  // same
   CUtensorMap ck;   // (64, page, 8, pages), box (64, page, 1, 1)
   CUtensorMap cv;
   CUtensorMap wk;   // (64, rows, 8, 1),  box (64, 128, 2, 1)
@@ -144,21 +155,43 @@ __device__ __forceinline__ int tiles_of(int L, int max_nc, bool report) {
   return seq_info(L, max_nc).nct + 1;
 }
 
+// Sequence of query i of a chunk: the last whose first token is not behind it.
+__device__ __forceinline__ int seq_of(const paged::Chunk& c, int i) {
+  int lo = 0, hi = c.S - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (c.q_start[mid] <= i) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
 // Tile prefix of S queries by one CTA of NT threads, each a run of queries:
-// out[i], out[S] = total, and the longest query in *longest.
+// out[i], out[S] = total, and the longest query in *longest.  lens, rows (may be
+// null): context length and table row of each query.
 template <int NT>
-__device__ __forceinline__ void plan_tiles(const int* ctx_len, int S, int max_nc, long long* out,
-                                           int* lens, int* longest, bool report) {
+__device__ __forceinline__ void plan_tiles(const Params& p, long long* out, int* lens, int* rows,
+                                           int* longest, bool report) {
   __shared__ long long wsum[NT / 32];
   __shared__ int wmax[NT / 32];
+  const int S = p.S;
   const int per = (S + NT - 1) / NT;
   const int i0 = min(static_cast<int>(threadIdx.x) * per, S), i1 = min(i0 + per, S);
   long long run = 0;
   int most = 0;
   for (int i = i0; i < i1; ++i) {
-    const int L = ctx_len[i];
-    const int n = tiles_of(L, max_nc, report);
-    if (lens != nullptr) lens[i] = L;
+    int L, row = i;
+    if (p.chunk.q_start != nullptr) {
+      row = seq_of(p.chunk, i);
+      const paged::Span sp = paged::span_of(p.chunk, row, false);
+      L = sp.L0 + min(max(i - sp.qs, 0), max(sp.n - 1, 0)) + 1;
+    } else {
+      L = p.ctx_len[i];
+    }
+    const int n = tiles_of(L, p.max_nc, report);
+    if (lens != nullptr) {
+      lens[i] = L;
+      rows[i] = row;
+    }
     out[i] = n;
     run += n;
     most = max(most, n);
@@ -192,13 +225,11 @@ __device__ __forceinline__ void plan_tiles(const int* ctx_len, int S, int max_nc
   __syncthreads();
 }
 
-__global__ void __launch_bounds__(1024)
-    plan_kernel(const int* ctx_len, int S, int max_nc, long long* seq_tile, const int* count) {
+__global__ void __launch_bounds__(1024) plan_kernel(const Params p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (count != nullptr) S = min(max(*count, 0), S);
   __shared__ int longest;
-  plan_tiles<1024>(ctx_len, S, max_nc, seq_tile, nullptr, &longest, true);
-  if (threadIdx.x == 0) seq_tile[S + 1] = longest;
+  plan_tiles<1024>(p, p.seq_tile, nullptr, nullptr, &longest, true);
+  if (threadIdx.x == 0) p.seq_tile[p.S + 1] = longest;
 }
 
 // largest s in [0, S) with first[s] <= x
@@ -234,11 +265,16 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// names the destination registers of a finished tcgen05.ld (see tmem_wait_ld_dep32)
-__device__ __forceinline__ void reg_dep16(uint32_t* r) {
-  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-               "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-               "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+template <int N>
+__device__ __forceinline__ void load_row(const float* src, float (&dst)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(src + i);
+    dst[i] = v.x;
+    dst[i + 1] = v.y;
+    dst[i + 2] = v.z;
+    dst[i + 3] = v.w;
+  }
 }
 
 __device__ __forceinline__ float redux_max(float x) {
@@ -268,34 +304,76 @@ __device__ __forceinline__ float sigmoid32(float x) {
   return __fdividef(1.f, 1.f + ex2_approx(-1.4426950408889634f * x));
 }
 
-// How a launch is split, the same in every CTA.
-struct Split {
-  long long N;   // tiles
-  int G;         // CTAs with tiles
-  bool whole;    // whole queries per CTA
-};
+// CTAs of a query of `t` tiles when each takes at most T (or, by rounding, a tile
+// more: what counts is that all CTAs find the same)
+__device__ __forceinline__ int parts_of(int t, float inv) {
+  return max(1, static_cast<int>(ceilf(static_cast<float>(t) * inv - 1e-3f)));
+}
+
+// With fewer queries than CTAs each CTA works for one query: query s is shared
+// by parts_of(t_s, T) CTAs, T the smallest for which all fit on the grid (found
+// by bisection, every warp for itself).  Sets the CTA's query, its part of n,
+// or n = 0 for a CTA that is left over.
+__device__ __forceinline__ void own_query(const long long* tiles, int S, int longest, int G, int cta,
+                                          int& s, int& part, int& n) {
+  const int lane = threadIdx.x & 31;
+  auto all_parts = [&](int T) -> int {
+    const float inv = __frcp_rn(static_cast<float>(T));
+    int x = 0;
+    for (int i = lane; i < S; i += 32) x += parts_of(static_cast<int>(tiles[i + 1] - tiles[i]), inv);
+    return __reduce_add_sync(0xffffffffu, x);
+  };
+  int lo = max(1, static_cast<int>((tiles[S] + G - 1) / G)), hi = max(lo, longest);
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (all_parts(mid) <= G) hi = mid; else lo = mid + 1;
+  }
+  const float inv = __frcp_rn(static_cast<float>(lo));
+  int before = 0;
+  n = 0;
+  for (int base = 0; base < S && n == 0; base += 32) {
+    const int i = base + lane;
+    const int m = i < S ? parts_of(static_cast<int>(tiles[i + 1] - tiles[i]), inv) : 0;
+    int x = m;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const int first = before + x - m;
+    const unsigned hit = __ballot_sync(0xffffffffu, m > 0 && cta >= first && cta < first + m);
+    if (hit != 0) {
+      const int l = __ffs(hit) - 1;
+      s = base + l;
+      n = __shfl_sync(0xffffffffu, m, l);
+      part = cta - __shfl_sync(0xffffffffu, first, l);
+    }
+    before += __shfl_sync(0xffffffffu, x, 31);
+  }
+}
 
 // ---------------------------------------------------------------------------
 // Merge of a query whose tiles n CTAs share, by all of them: CTA i of the n
-// takes the rows (heads) [64 i / n, 64 (i + 1) / n) of all n partials, once
-// all have been written (a counter per query; a CTA waits only for those that
-// share its first or last query, and only after its own tiles).  First every
-// warp finds the weights w_f = l_f 2^(m_f - M) / L of its rows' splits, lane =
-// split; then lane l adds up value columns 128 q + 4 l .. + 3 (a partial row is
-// four 16-byte loads a lane, four splits in flight).  With fewer rows than
-// warps, several warps share a row's splits and add up through shared memory.
+// takes the chunks (16 heads x 32 value columns) [64 i / n, 64 (i + 1) / n) of
+// all n partials, once all have been written (a counter per query; a CTA waits
+// only for those that share its first or last query, and only after its own
+// tiles).  The weights w = l_f 2^(m_f - M) / L of all splits and heads are found
+// in shared memory first; then a warp adds up a chunk, lane l holding heads
+// 4 q + l / 8 and columns 4 (l % 8) .. + 3 (a chunk of a split is four 16-byte
+// loads a lane, four splits in flight).  With fewer chunks than warps, several
+// warps share a chunk's splits and add up through shared memory.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void merge_query(const Params& p, int s, int c0, int n, uint8_t* smem,
                                             int warp, int lane) {
   const int i = static_cast<int>(blockIdx.x) - c0;
-  const int h0 = kHeads * i / n, nr = kHeads * (i + 1) / n - h0;
+  const int k0 = 64 * i / n, nk = 64 * (i + 1) / n - k0;
   __shared__ int late;
   if (threadIdx.x == 0) {
     const uint64_t t0 = globaltimer_ns();
     late = 0;
     for (uint32_t k = 1;; ++k) {
       unsigned v;
-      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p.arrived + s) : "memory");
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p.arrived + c0) : "memory");
       if (v >= static_cast<unsigned>(n)) break;
       if ((k & 63u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) {
         record_error(DEVERR_TIMEOUT, 72);
@@ -303,63 +381,99 @@ __device__ __forceinline__ void merge_query(const Params& p, int s, int c0, int 
         break;
       }
     }
+    fence_proxy_async_all();   // the partials were written by bulk copies
   }
   __syncthreads();
-  if (nr > 0 && !late) {
-    const int share = nr < kWarps ? kWarps / nr : 1;           // warps per row
-    const int part = warp % share, slot0 = warp / share, rows = kWarps / share;
-    float* add = reinterpret_cast<float*>(smem + kSmemRing);    // [warps][512]
-    float* wt = reinterpret_cast<float*>(smem + kSmemQ);        // [warps][grid]
-    float* w = wt + warp * gridDim.x;
-    for (int r0 = 0; r0 < nr; r0 += rows) {
-      const int r = r0 + slot0;
-      const bool mine = slot0 < rows && r < nr;
-      const int h = h0 + r;
-      const size_t row = static_cast<size_t>(s) * kHeads + h;
+  if (nk > 0 && !late) {
+    const int share = nk < kWarps ? kWarps / nk : 1;            // warps per chunk
+    const int part = warp % share, slot0 = warp / share, chunks = kWarps / share;
+    const float* po = p.ws_o + static_cast<size_t>(c0 + s) * kHeads * kDim + 4 * lane;
+    float* wt = reinterpret_cast<float*>(smem + kSmemQ);        // [n][64] m, then weights
+    float* add = wt + static_cast<size_t>(n) * kHeads;          // [warps][512]
+    // m and l of every split: head 2 lane, 2 lane + 1
+    const float2* ml = reinterpret_cast<const float2*>(p.ws_ml + static_cast<size_t>(c0 + s) * 128);
+    float2 M = make_float2(-INFINITY, -INFINITY), L = make_float2(0.f, 0.f);
+    if (n <= 4) {   // few splits: every warp for itself, without barriers
+      float2 m[4], l[4];
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        m[f] = f < n ? __ldcg(ml + 64 * f + lane) : make_float2(-INFINITY, -INFINITY);
+        l[f] = f < n ? __ldcg(ml + 64 * f + 32 + lane) : make_float2(0.f, 0.f);
+        M.x = fmaxf(M.x, m[f].x);
+        M.y = fmaxf(M.y, m[f].y);
+      }
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        l[f].x *= ex2_approx(m[f].x - M.x);
+        l[f].y *= ex2_approx(m[f].y - M.y);
+        L.x += l[f].x;
+        L.y += l[f].y;
+      }
+      float2* w = reinterpret_cast<float2*>(wt) + warp * 4 * 32;
+      wt = reinterpret_cast<float*>(w);
+      add = reinterpret_cast<float*>(smem + kSmemRing);
+#pragma unroll
+      for (int f = 0; f < 4; ++f)
+        w[32 * f + lane] = make_float2(l[f].x / L.x, l[f].y / L.y);
+      __syncwarp();
+    } else {
+      float2* w = reinterpret_cast<float2*>(wt);
+      for (int f = warp; f < n; f += kWarps) w[32 * f + lane] = __ldcg(ml + 64 * f + lane);
+      __syncthreads();
+      for (int f = 0; f < n; ++f) {
+        const float2 m = w[32 * f + lane];
+        M.x = fmaxf(M.x, m.x);
+        M.y = fmaxf(M.y, m.y);
+      }
+      __syncthreads();
+      for (int f = warp; f < n; f += kWarps) {
+        const float2 m = w[32 * f + lane], l = __ldcg(ml + 64 * f + 32 + lane);
+        w[32 * f + lane] = make_float2(l.x * ex2_approx(m.x - M.x), l.y * ex2_approx(m.y - M.y));
+      }
+      __syncthreads();
+      for (int f = 0; f < n; ++f) {
+        const float2 x = w[32 * f + lane];
+        L.x += x.x;
+        L.y += x.y;
+      }
+      __syncthreads();
+      for (int f = warp; f < n; f += kWarps) {
+        const float2 x = w[32 * f + lane];
+        w[32 * f + lane] = make_float2(x.x / L.x, x.y / L.y);
+      }
+      __syncthreads();
+    }
+    for (int r0 = 0; r0 < nk; r0 += chunks) {
+      const int k = k0 + r0 + slot0;
+      const bool mine = slot0 < chunks && r0 + slot0 < nk;
+      const int h0 = 16 * (k >> 4) + (lane >> 3);               // heads h0 + 4 q
+      const size_t at = (static_cast<size_t>(s) * kHeads + h0) * kDim + 32 * (k & 15) + 4 * (lane & 7);
       float acc[16];
 #pragma unroll
       for (int t = 0; t < 16; ++t) acc[t] = 0.f;
       uint2 gv[4];
       if (mine) {
-        const float* ml = p.ws_ml + static_cast<size_t>(c0 + s) * 128 + h;
-        const uint2* gp = reinterpret_cast<const uint2*>(p.g + row * kDim + 4 * lane);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) gv[q] = __ldg(gp + 32 * q);
-        float M = -INFINITY, L = 0.f;
-        for (int f = lane; f < n; f += 32) {
-          const float m = __ldcg(ml + 128 * f);
-          w[f] = m;
-          M = fmaxf(M, m);
-        }
-        M = redux_max(M);
-        const float mu = M == -INFINITY ? 0.f : M;
-        for (int f = lane; f < n; f += 32) {
-          const float x = __ldcg(ml + 128 * f + 64) * ex2_approx(w[f] - mu);
-          w[f] = x;
-          L += x;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-        __syncwarp();
-        const float inv = 1.f / L;
-        const float4* po = reinterpret_cast<const float4*>(
-                               p.ws_o + (static_cast<size_t>(c0 + s) * kHeads + h) * kDim) + lane;
+        for (int q = 0; q < 4; ++q)
+          gv[q] = __ldg(reinterpret_cast<const uint2*>(p.g + at + 4 * q * kDim));
 #pragma unroll 1
         for (int f0 = part; f0 < n; f0 += 4 * share) {
           float4 x[4][4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const int f = min(f0 + u * share, n - 1);
+            const int f = f0 + u * share;
+            const float4* src = reinterpret_cast<const float4*>(
+                po + static_cast<size_t>(f) * kHeads * kDim + 512 * k);
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              x[u][q] = __ldcg(po + static_cast<size_t>(f) * (kHeads * kDim / 4) + 32 * q);
+              x[u][q] = f < n ? __ldcg(src + 32 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
           }
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const int f = f0 + u * share;
-            const float wf = f < n ? w[f] * inv : 0.f;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
+              const float wf = f < n ? wt[64 * f + h0 + 4 * q] : 0.f;
               acc[4 * q] = fmaf(wf, x[u][q].x, acc[4 * q]);
               acc[4 * q + 1] = fmaf(wf, x[u][q].y, acc[4 * q + 1]);
               acc[4 * q + 2] = fmaf(wf, x[u][q].z, acc[4 * q + 2]);
@@ -373,7 +487,7 @@ __device__ __forceinline__ void merge_query(const Params& p, int s, int c0, int 
         if (mine && part > 0) {
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<float4*>(add + warp * kDim + 128 * q + 4 * lane) =
+            *reinterpret_cast<float4*>(add + warp * 512 + 128 * q + 4 * lane) =
                 make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
         }
         __syncthreads();
@@ -382,7 +496,7 @@ __device__ __forceinline__ void merge_query(const Params& p, int s, int c0, int 
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const float4 x =
-                  *reinterpret_cast<const float4*>(add + (warp + v) * kDim + 128 * q + 4 * lane);
+                  *reinterpret_cast<const float4*>(add + (warp + v) * 512 + 128 * q + 4 * lane);
               acc[4 * q] += x.x;
               acc[4 * q + 1] += x.y;
               acc[4 * q + 2] += x.z;
@@ -392,13 +506,13 @@ __device__ __forceinline__ void merge_query(const Params& p, int s, int c0, int 
         }
       }
       if (mine && part == 0) {
-        uint2* op = reinterpret_cast<uint2*>(p.out + row * kDim + 4 * lane);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          op[32 * q] = make_uint2(pack_bf16x2(acc[4 * q] * sigmoid32(bf16lo_to_f32(gv[q].x)),
-                                              acc[4 * q + 1] * sigmoid32(bf16hi_to_f32(gv[q].x))),
-                                  pack_bf16x2(acc[4 * q + 2] * sigmoid32(bf16lo_to_f32(gv[q].y)),
-                                              acc[4 * q + 3] * sigmoid32(bf16hi_to_f32(gv[q].y))));
+          *reinterpret_cast<uint2*>(p.out + at + 4 * q * kDim) =
+              make_uint2(pack_bf16x2(acc[4 * q] * sigmoid32(bf16lo_to_f32(gv[q].x)),
+                                     acc[4 * q + 1] * sigmoid32(bf16hi_to_f32(gv[q].x))),
+                         pack_bf16x2(acc[4 * q + 2] * sigmoid32(bf16lo_to_f32(gv[q].y)),
+                                     acc[4 * q + 3] * sigmoid32(bf16hi_to_f32(gv[q].y))));
       }
     }
   }
@@ -409,9 +523,9 @@ __device__ __forceinline__ void merge_query(const Params& p, int s, int c0, int 
     unsigned old;
     asm volatile("atom.add.relaxed.gpu.global.u32 %0, [%1], 1;"
                  : "=r"(old)
-                 : "l"(p.arrived + s)
+                 : "l"(p.arrived + c0)
                  : "memory");
-    if (old == 2u * n - 1) p.arrived[s] = 0u;
+    if (old == 2u * n - 1) p.arrived[c0] = 0u;
   }
 }
 
@@ -454,6 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&maps.cv);
     tma_prefetch_desc(&maps.wk);
     tma_prefetch_desc(&maps.wv);
+    tma_prefetch_desc(&maps.g);
+    tma_prefetch_desc(&maps.out);
   }
   if (warp == kProducers) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
@@ -461,16 +577,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
   }
   // The plan, here for up to kInlineSeqs queries.  The kernel may have been
-  // launched while the one in front of it still runs: it waits before it reads
-  // anything that one writes.
-  const bool inl = p0.S <= kInlineSeqs;
-  if (inl && p.plan_early)
-    plan_tiles<kThreads>(p.ctx_len, p.S, p.max_nc, sT, sL, &longest, blockIdx.x == 0);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (p.count != nullptr) p.S = min(max(*p.count, 0), p0.S);
-  if (inl && !p.plan_early)
-    plan_tiles<kThreads>(p.ctx_len, p.S, p.max_nc, sT, sL, &longest, blockIdx.x == 0);
-  if (!inl) {
+  // launched while the one in front of it still runs.
+  const bool inl = p.S <= kInlineSeqs;
+  int* sRow = reinterpret_cast<int*>(smem + kSmemRow);
+  if (!p.only_window) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (inl) {
+    if (p.chunk.q_start != nullptr) p.S = min(max(p.chunk.q_start[p.chunk.S], 0), p.S);
+    plan_tiles<kThreads>(p, sT, sL, sRow, &longest, blockIdx.x == 0);
+  } else {
     if (threadIdx.x == 0) longest = static_cast<int>(p.seq_tile[p.S + 1]);
     __syncthreads();
   }
@@ -478,20 +592,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const long long* tiles = inl ? sT : p.seq_tile;
   const int* lens = inl ? sL : p.ctx_len;
-  Split sp;
-  sp.N = tiles[p.S];
-  sp.G = static_cast<int>(min(static_cast<long long>(gridDim.x), max(sp.N, 1LL)));
-  const int per = (p.S + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
-  sp.whole = static_cast<long long>(longest) * per <=
-             decode::div_nn(sp.N + gridDim.x - 1, gridDim.x) + kWholeTiles;
+  // How the tiles are split: whole queries per CTA where that costs little, else
+  // one query per CTA where there are fewer queries than CTAs, else an even cut
+  // of all tiles laid end to end.
+  const long long N = tiles[p.S];
+  const int grid = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
+  const bool whole = static_cast<long long>(longest) * ((p.S + grid - 1) / grid) <=
+                     decode::div_nn(N + grid - 1, grid) + kWholeTiles;
+  const bool own = !whole && p.S < grid;
+  const int G = static_cast<int>(min(static_cast<long long>(grid), max(N, 1LL)));   // even cut
   long long A0 = 0, A1 = 0;
-  if (sp.whole) {
-    A0 = tiles[decode::div_nn(static_cast<long long>(p.S) * blockIdx.x, gridDim.x)];
-    A1 = tiles[decode::div_nn(static_cast<long long>(p.S) * (blockIdx.x + 1), gridDim.x)];
-  } else if (static_cast<int>(blockIdx.x) < sp.G) {
-    A0 = decode::div_nn(sp.N * blockIdx.x, sp.G);
-    A1 = decode::div_nn(sp.N * (blockIdx.x + 1), sp.G);
+  int mine = 0, part = 0, parts = 0;   // own: this CTA's query
+  if (whole) {
+    A0 = tiles[decode::div_nn(static_cast<long long>(p.S) * cta, grid)];
+    A1 = tiles[decode::div_nn(static_cast<long long>(p.S) * (cta + 1), grid)];
+  } else if (own) {
+    own_query(tiles, p.S, longest, grid, cta, mine, part, parts);
+    if (parts > 0) {
+      const int t = static_cast<int>(tiles[mine + 1] - tiles[mine]);
+      A0 = tiles[mine] + t * part / parts;
+      A1 = tiles[mine] + t * (part + 1) / parts;
+    }
+  } else if (cta < G) {
+    A0 = decode::div_nn(N * cta, G);
+    A1 = decode::div_nn(N * (cta + 1), G);
   }
+  auto owner = [&](long long x) -> int {   // even cut: CTA of tile x
+    return static_cast<int>(decode::div_nn((x + 1) * G + N - 1, N)) - 1;
+  };
   if (A0 < A1) {  // uniform across the CTA
 
   // Segments: maximal runs of this CTA's tiles inside one query.
@@ -505,16 +633,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int boxes = kKeyTile >> p.page_shift;
     const int bx = lane & (boxes - 1), slab = lane / boxes;
     const uint32_t boff = slab * kSlab + bx * (kSlab / boxes);
-    uint32_t u = 0, quse = 0;   // u: rounds of the ring
+    uint32_t ua = 0, ub = 0, quse = 0;   // uses of stages 0, 1 and 2, 3 so far
     bool ok = true;
+    bool waited = !p.only_window;
     // The eight slabs of a tile: entries of the page `pg` of this lane's box, or
     // (pg < 0) the window rows from y on
     auto load = [&](const CUtensorMap* map, int pg, int y) {
+      if (pg < 0 && !waited) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        waited = true;
+      }
 #pragma unroll
       for (int i = 0; i < kStages / kProducers; ++i) {
         const int st = kProducers * i + me;
         if (lane == 0) {
-          ok = ok && mbar_wait(bar(B_EMPTY + st), (u & 1) ^ 1, abort_flag, kWaitLimitNs, 40);
+          ok = ok && mbar_wait(bar(B_EMPTY + st), ((st < 2 ? ua : ub) & 1) ^ 1, abort_flag,
+                               kWaitLimitNs, 40);
           if (ok) mbar_expect_tx(bar(B_FULL + st), kStage);
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -525,7 +659,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         else if (ok && pg < 0 && lane == 0)
           decode::tma_load_4d_dec(sRing + st * kStage, map, bar(B_FULL + st), 0, y, 2 * st, 0);
       }
-      ++u;
+      ++ua;
+      ++ub;
     };
     long long x = A0;
     for (int s = s_first; x < A1 && ok; ++s) {
@@ -544,8 +679,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
       ++quse;
-      const int* prow = p.table + (p.row_of != nullptr ? p.row_of[s] : s) * p.table_ld;
-      const int win = p.win_row != nullptr ? p.win_row[s] : s * kWin;
+      const int trow = inl ? sRow[s] : s;
+      const int* prow = p.table + trow * p.table_ld;
+      const int win = p.chunk.q_start != nullptr ? s + paged::kPad * trow : s * kWin;
       auto page_of = [&](int j) -> int {
         return j < si.nct ? box_page(p, prow, si.nc, j, bx) : -1;
       };
@@ -558,7 +694,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         pg = pg1;
         pg1 = pg2;
       }
+      if (j0 == 0 && seg_end == tiles[s + 1]) {   // a whole query: its gate, into stages 0 and 1
+        if (lane == 0) {
+          ok = ok && mbar_wait(bar(B_EMPTY + me), (ua & 1) ^ 1, abort_flag, kWaitLimitNs, 43);
+          if (ok) {
+            mbar_expect_tx(bar(B_FULL + me), kStage);
+            decode::tma_load_4d_dec(sRing + me * kStage, &maps.g, bar(B_FULL + me), 0, s * kHeads,
+                                    4 * me, 0);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        ++ua;
+      }
       x = seg_end;
+    }
+    // The last copies are out: bring the gate of the rows that this CTA will merge
+    // into L2 (about the heads of its chunks: 64 part / parts ..).
+    if (own && parts > 1 && me == 0 && lane == 0) {
+      const int h0 = kHeads * part / parts, h1 = (kHeads * (part + 1) + parts - 1) / parts;
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                       p.g + (static_cast<size_t>(mine) * kHeads + h0) * kDim),
+                   "r"(static_cast<uint32_t>(min(h1, kHeads) - h0) * kDim * 2)
+                   : "memory");
     }
   } else if (warp == kProducers) {
     // ------------------------------------------------------------ MMA issuer
@@ -568,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // take from shared memory) against 115 under a branch on the lane number.
     // `ok` is uniform; after a failed wait the loops run on without waiting.
     bool ok = true;
-    uint32_t ring = 0, quse = 0, sidx = 0, pvidx = 0, nseg = 0;   // ring: rounds
+    uint32_t ua = 0, ub = 0, quse = 0, sidx = 0, pvidx = 0, nseg = 0;   // as the producers'
     const uint32_t idesc_s = idesc_bf16_f32(128, 64, false, false);
     const uint32_t idesc_o = idesc_bf16_f32(128, 64, true, true);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -582,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t dS = tm + (buf ? kTmemS1 : kTmemS0);
 #pragma unroll 1
       for (int st = 0; st < kStages; ++st) {
-        wait(B_FULL + st, ring & 1, 51);
+        wait(B_FULL + st, (st < 2 ? ua : ub) & 1, 51);
         tc_fence_after();
         const uint64_t ad = sdesc_sw128(sRing + st * kStage, 16, 1024);
         const uint64_t bd = sdesc_sw128(sQ + st * 2 * kQSlab, 16, 1024);
@@ -596,7 +753,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
-      ++ring;
+      ++ua;
+      ++ub;
       ++sidx;
     };
     auto issue_pv = [&](bool first, int valid) {
@@ -605,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int ksteps = (valid + 15) >> 4;
 #pragma unroll 1
       for (int c = 0; c < kStages; ++c) {   // 128 value columns each
-        wait(B_FULL + c, ring & 1, 54);
+        wait(B_FULL + c, (c < 2 ? ua : ub) & 1, 54);
         if (ok && (valid & 15) != 0) {
           clear_rows(smem + kSmemRing + c * kStage, valid, lane);
           fence_proxy_async_smem();               // read next by the tensor core
@@ -631,7 +789,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
-      ++ring;
+      ++ua;
+      ++ub;
       ++pvidx;
     };
     auto commit = [&](int b) {
@@ -654,9 +813,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j + 2 == j1) commit(B_QEMPTY);
         }
         issue_pv(j == j0, j < si.nct ? min(kKeyTile, si.nc - j * kKeyTile)
-                          : p.win_row != nullptr ? kWin : min(si.L, kWin));
+                          : p.chunk.q_start != nullptr ? kWin : min(si.L, kWin));
       }
       commit(B_OFULL);
+      if (j0 == 0 && seg_end == tiles[s + 1]) {   // the gate: its phases, too, pass in order
+        wait(B_FULL, ua & 1, 55);
+        wait(B_FULL + 1, ua & 1, 55);
+        ++ua;
+      }
       ++nseg;
       x = seg_end;
     }
@@ -674,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* smax = reinterpret_cast<float*>(smem + kSmemMax) + 128 * half;
     float* ssum = reinterpret_cast<float*>(smem + kSmemSum) + 128 * half;
     volatile int* flag = reinterpret_cast<volatile int*>(smem + kSmemFlag) + 4 * half;
-    uint32_t sidx = 0, pvidx = 0, nseg = 0;
+    uint32_t sidx = 0, pvidx = 0, nseg = 0, ua = 0;
     // A failed wait leaves `ok` false and the loops running (without waiting),
     // so that the four warps of a half keep meeting at their barrier.
     bool ok = true;
@@ -703,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++sidx;
         bool valid;
         if (j < si.nct) valid = j * kKeyTile + key < si.nc;
-        else if (p.win_row != nullptr) valid = key >= kWin - si.L;   // positions >= 0
+        else if (p.chunk.q_start != nullptr) valid = key >= kWin - si.L;   // positions >= 0
         else valid = (si.L >= kWin) || (key < si.L);
 
         // d = scale s - m by head; does any pass the bound?
@@ -803,7 +967,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---------------------------------------------------------- end of the segment
       const bool direct = j0 == 0 && seg_end == tiles[s + 1];   // the whole query is here
-      const size_t hrow = static_cast<size_t>(s) * kHeads + 32 * half;
       const float lw = lanes_sum32(lsum);
       ssum[32 * wq + lane] = lw;
       named_bar_sync(1 + half, 128);
@@ -811,78 +974,117 @@ __global__ void __launch_bounds__(kThreads, 1)
       mrow[32 + lane] = l > 0.f ? 1.f / l : 0.f;
       __syncwarp();
       named_bar_sync(1 + half, 128);   // ssum is written again by the next segment
-      // 16 heads of 128 value columns at a time, in a short loop: this code runs
-      // once a segment, and what it costs is above all its way into the
+      ua += 2 * (j1 - j0);             // stage 0: K and V of every tile
+      // 8 or 16 heads of 128 value columns at a time, in short loops: this code
+      // runs once a segment, and much of what it costs is its way into the
       // instruction cache.
       if (direct) {
-        // gate: 16-byte chunk lane % 4 of rows (heads) lane / 4 and + 8, value columns 128 c + 32 wq
-        const size_t goff = (hrow + (lane >> 2)) * kDim + 32 * wq + 8 * (lane & 3);
-        // this warp's 1 KB of the P^T buffer: [16 heads][32 value columns] bf16
-        uint8_t* stage = smem + kSmemPT + 1024 * sw;
-        uint4 ga = __ldg(reinterpret_cast<const uint4*>(p.g + goff));
-        uint4 gb = __ldg(reinterpret_cast<const uint4*>(p.g + goff + 8 * kDim));
+        // out = gate O / l in place of the gate ([8 slabs][64 heads][64] swizzled)
         if (ok) ok = mbar_wait_warp(bar(B_OFULL), nseg & 1, abort_flag, kWaitLimitNs, 62);
+        // Only now: O is complete, so every earlier use of the stages has landed,
+        // and the parity names the gate's use (before, the parity of a use two
+        // back would let the wait pass).
+        if (ok)
+          ok = mbar_wait_warp(bar(B_FULL), ua & 1, abort_flag, kWaitLimitNs, 63) &&
+               mbar_wait_warp(bar(B_FULL + 1), ua & 1, abort_flag, kWaitLimitNs, 63);
+        ++ua;
         tc_fence_after();
+        // 16 heads x 32 value columns at a time through this warp's 2 KB of the P^T
+        // buffer: from TMEM a thread has one column of many heads; it then takes 16
+        // columns of one head, so that gate and output move 8 bytes at a time
+        // (2-byte accesses took 4.9 us a query)
+        float* stage = reinterpret_cast<float*>(smem + kSmemPT) + 512 * sw;
+        float inv[32];
+        load_row<32>(mrow + 32, inv);
+        const int hr = lane >> 1, rot = (lane >> 1) & 3;     // row; order of its 4-column groups
+        const int col0 = 32 * (wq & 1) + 16 * (lane & 1);    // within a 64-wide slab
+        uint8_t* grow = smem + kSmemRing + (wq >> 1) * kQSlab + (32 * half + hr) * 128;
 #pragma unroll 1
-        for (int i = 0; i < 8; ++i) {      // heads 16 (i & 1), value columns 128 (i >> 1)
-          uint32_t o[16];
-          tmem_ld16(tl + kTmemO + 64 * (i >> 1) + 16 * (i & 1), o);
-          *reinterpret_cast<uint4*>(stage + 16 * lane) = ga;
-          *reinterpret_cast<uint4*>(stage + 512 + 16 * lane) = gb;
-          const size_t at = goff + 16 * (i & 1) * kDim + 128 * (i >> 1);
-          if (i < 7) {
-            const size_t nx = goff + 16 * ((i + 1) & 1) * kDim + 128 * ((i + 1) >> 1);
-            ga = __ldg(reinterpret_cast<const uint4*>(p.g + nx));
-            gb = __ldg(reinterpret_cast<const uint4*>(p.g + nx + 8 * kDim));
-          }
-          tmem_wait_ld();
-          reg_dep16(o);
-          __syncwarp();
-          const float* inv = mrow + 32 + 16 * (i & 1);
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tl + kTmemO + 64 * c, o);
+          tmem_wait_ld_dep32(o);
 #pragma unroll
-          for (int h = 0; h < 16; ++h) {
-            uint16_t* e = reinterpret_cast<uint16_t*>(stage + 64 * h) + lane;
-            const float gate = sigmoid32(__uint_as_float(static_cast<uint32_t>(*e) << 16));
-            const __nv_bfloat16 v = __float2bfloat16_rn(__uint_as_float(o[h]) * inv[h] * gate);
-            *e = *reinterpret_cast<const uint16_t*>(&v);
+          for (int hb = 0; hb < 2; ++hb) {
+#pragma unroll
+            for (int h = 0; h < 16; ++h)
+              stage[32 * h + lane] = __uint_as_float(o[16 * hb + h]) * inv[16 * hb + h];
+            __syncwarp();
+            float4 v[4];
+            uint2 gv[4];
+            uint8_t* gr = grow + c * 2 * kQSlab + 16 * hb * 128;
+            auto gat = [&](int q) -> uint2* {   // 8 bytes: 4 columns from col0 + 4 (q ^ rot)
+              const int col = col0 + 4 * (q ^ rot);
+              return reinterpret_cast<uint2*>(gr + (((col >> 3) ^ (hr & 7)) << 4) + 2 * (col & 7));
+            };
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              v[q] = *reinterpret_cast<const float4*>(stage + 32 * hr + 16 * (lane & 1) +
+                                                      4 * (q ^ rot));
+              gv[q] = *gat(q);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *gat(q) = make_uint2(pack_bf16x2(v[q].x * sigmoid_fast(bf16lo_to_f32(gv[q].x)),
+                                               v[q].y * sigmoid_fast(bf16hi_to_f32(gv[q].x))),
+                                   pack_bf16x2(v[q].z * sigmoid_fast(bf16lo_to_f32(gv[q].y)),
+                                               v[q].w * sigmoid_fast(bf16hi_to_f32(gv[q].y))));
           }
-          __syncwarp();
-          *reinterpret_cast<uint4*>(p.out + at) = *reinterpret_cast<const uint4*>(stage + 16 * lane);
-          *reinterpret_cast<uint4*>(p.out + at + 8 * kDim) =
-              *reinterpret_cast<const uint4*>(stage + 512 + 16 * lane);
-          __syncwarp();
         }
-        named_bar_sync(3, 32 * kSoftWarps);   // the next query's P^T overwrites the stages
+        fence_proxy_async_smem();
+        named_bar_sync(3, 32 * kSoftWarps);
+        if (sw == 0 && lane == 0) {
+          if (ok) {
+            prefill3::tma_store_4d(&maps.out, sRing, 0, s * kHeads, 0, 0);
+            prefill3::tma_store_4d(&maps.out, sRing + kStage, 0, s * kHeads, 4, 0);
+          }
+          bulk_commit();
+          bulk_wait_read_all();
+          mbar_arrive(bar(B_EMPTY));
+          mbar_arrive(bar(B_EMPTY + 1));
+        }
       } else {
         const size_t slot = static_cast<size_t>(blockIdx.x) + s;
-        float* wo = p.ws_o + (slot * kHeads + 32 * half) * kDim + key;
         if (wq == 0) {
           p.ws_ml[slot * 128 + 32 * half + lane] = m;
           p.ws_ml[slot * 128 + 64 + 32 * half + lane] = l;
         }
         if (ok) ok = mbar_wait_warp(bar(B_OFULL), nseg & 1, abort_flag, kWaitLimitNs, 62);
         tc_fence_after();
+        float* wo = p.ws_o + slot * kHeads * kDim + (2 * half * 16 + wq) * 512;
+        float inv[32];
+        load_row<32>(mrow + 32, inv);      // before the stores, which it could not pass
 #pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-          uint32_t o[16];
-          tmem_ld16(tl + kTmemO + 64 * (i >> 1) + 16 * (i & 1), o);
-          tmem_wait_ld();
-          reg_dep16(o);
-          const float* inv = mrow + 32 + 16 * (i & 1);
-          float* dst = wo + 16 * (i & 1) * kDim + 128 * (i >> 1);
+        for (int i = 0; i < 2; ++i) {      // value columns 256 i + key and 256 i + 128 + key
+          uint32_t o[64];
+          tmem_ld32(tl + kTmemO + 128 * i, o);
+          tmem_ld32(tl + kTmemO + 128 * i + 64, o + 32);
+          tmem_wait_ld_dep32(o);
+          reg_dep32(o + 32);
+          float* dst = wo + 8 * i * 512 + lane;
 #pragma unroll
-          for (int h = 0; h < 16; ++h) dst[h * kDim] = __uint_as_float(o[h]) * inv[h];
+          for (int h = 0; h < 32; ++h) {
+            dst[(h >> 4) * 16 * 512 + 32 * (h & 15)] = __uint_as_float(o[h]) * inv[h];
+            dst[(h >> 4) * 16 * 512 + 4 * 512 + 32 * (h & 15)] = __uint_as_float(o[32 + h]) * inv[h];
+          }
         }
         // the partial is written: one arrival for the CTAs that share the query
         named_bar_sync(3, 32 * kSoftWarps);
         if (sw == 0 && lane == 0)
-          asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.arrived + s) : "memory");
+          asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(
+                           p.arrived + (own ? cta - part : owner(tiles[s])))
+                       : "memory");
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_OFREE));
       ++nseg;
       x = seg_end;
+    }
+    if (sw == 0 && lane == 0) {   // outputs stored above
+      bulk_wait_all();
+      fence_proxy_async_all();
     }
   }
 
@@ -929,10 +1131,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
   };
-  if (!sp.whole && A0 < A1) {
-    auto owner = [&](long long x) -> int {   // CTA of tile x
-      return static_cast<int>(decode::div_nn((x + 1) * sp.G + sp.N - 1, sp.N)) - 1;
-    };
+  if (own) {
+    if (parts > 1) merge_query(p, mine, cta - part, parts, smem, warp, lane);
+  } else if (!whole && A0 < A1) {
     // the first and the last query of this CTA may be shared with others
     const int sa = find_seq(tiles, p.S, A0), sb = find_seq(tiles, p.S, A1 - 1);
     for (int s = sa; s <= sb; s += max(sb - sa, 1)) {

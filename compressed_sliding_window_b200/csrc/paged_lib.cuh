@@ -80,6 +80,12 @@ long long entry_units(int S, int N) {
   return N / hca::paged::kBlk + static_cast<long long>(hca::paged::kUnitsExtra) * S;
 }
 
+// The zero-filled head of a workspace, the same for every call: grid barrier,
+// counters of the merges.
+constexpr int kMaxGrid = 960;
+constexpr size_t kHeadBytes = 256 + 4 * kMaxGrid;
+static_assert(kHeadBytes % 256 == 0, "what follows is aligned");
+
 // One query at a time, split over the keys: the rest of `prm`, maps, launches.
 hca_status_t paged_attend(const hca::paged::Cache& c, const hca_bf16* q, const hca_bf16* g,
                           hca_bf16* out, const hca_bf16* wk, const hca_bf16* wv,
@@ -91,8 +97,9 @@ hca_status_t paged_attend(const hca::paged::Cache& c, const hca_bf16* q, const h
   const int slots = sms + prm.S;
   prm.max_nc = c.num_pages > 0 ? c.max_pages << c.page_shift : 0;
   prm.gsync = reinterpret_cast<unsigned long long*>(ws);
+  if (sms > kMaxGrid) return HCA_ERR_UNSUPPORTED;
   prm.arrived = reinterpret_cast<unsigned*>(ws + 256);
-  ws += 256 + align256(static_cast<size_t>(prm.S) * 4);
+  ws += kHeadBytes;
   prm.ws_o = reinterpret_cast<float*>(ws);
   prm.ws_ml = reinterpret_cast<float*>(ws + D::ws_o_bytes(slots));
   prm.seq_tile = reinterpret_cast<long long*>(ws + align256(D::ws_bytes(slots)));
@@ -105,6 +112,8 @@ hca_status_t paged_attend(const hca::paged::Cache& c, const hca_bf16* q, const h
   D::Maps maps;
   const uint32_t box = 1u << c.page_shift;
   bool ok = make_map4(&maps.q, q, static_cast<uint64_t>(prm.S) * HCA_NUM_HEADS, 1, 64, 8) &&
+            make_map4(&maps.g, g, static_cast<uint64_t>(prm.S) * HCA_NUM_HEADS, 1, 64, 4) &&
+            make_map4(&maps.out, out, static_cast<uint64_t>(prm.S) * HCA_NUM_HEADS, 1, 64, 4) &&
             make_map4(&maps.wk, wk, win_rows, 1, 128, 2) &&
             make_map4(&maps.wv, wv, win_rows, 1, 128, 2);
   if (ok && c.num_pages > 0) {
@@ -121,7 +130,7 @@ hca_status_t paged_attend(const hca::paged::Cache& c, const hca_bf16* q, const h
       }) != cudaSuccess)
     return HCA_ERR_CUDA;
   if (prm.S > D::kInlineSeqs) {
-    D::plan_kernel<<<1, 1024, 0, stream>>>(prm.ctx_len, prm.S, prm.max_nc, prm.seq_tile, prm.count);
+    D::plan_kernel<<<1, 1024, 0, stream>>>(prm);
     if (cudaGetLastError() != cudaSuccess) return HCA_ERR_CUDA;
   }
   // cooperative: CTAs that share a query wait for one another
@@ -163,12 +172,14 @@ hca_status_t attend_args(const hca_bf16* q, const hca_bf16* g, const hca_bf16* o
 #define HCA_SPLIT_TOKENS 40
 #endif
 constexpr int kSplitTokens = HCA_SPLIT_TOKENS;
+static_assert(kSplitTokens <= 128 || HCA_SPLIT_TOKENS == 1000,
+              "a block that the chunk completes must not become visible in it");
 constexpr int kMaxChunkSeqs = 4096;
 
 struct PagedPrefillLayout {
   bool split;   // one query at a time, split over the keys; else four positions at a time
   int items;    // room in the item list
-  size_t decode, len, row_of, win_row, list, tail16, tail, scratch, count, raw_k, raw_v, total;
+  size_t list, tail16, tail, scratch, count, raw_k, raw_v, total;
 };
 
 PagedPrefillLayout paged_prefill_layout(int S, int N, int clusters) {
@@ -182,13 +193,10 @@ PagedPrefillLayout paged_prefill_layout(int S, int N, int clusters) {
   L.split = N <= kSplitTokens;
   // sum of ceil(n / 4) over S sequences with N tokens
   L.items = static_cast<int>((static_cast<long long>(N) + 3LL * S) / 4);
-  L.count = take(4);
-  if (L.split) {
-    L.decode = take(hca_paged_decode_workspace_size(N));
-    L.len = take(static_cast<size_t>(N) * 4);
-    L.row_of = take(static_cast<size_t>(N) * 4);
-    L.win_row = take(static_cast<size_t>(N) * 4);
-  } else {
+  // the split form's workspace is at its start, and its head is nobody else's
+  take(L.split ? hca_paged_decode_workspace_size(N) : kHeadBytes);
+  if (!L.split) {
+    L.count = take(4);
     L.list = take(static_cast<size_t>(L.items) * 16);
     L.tail16 = take(static_cast<size_t>(S) * 4);
     L.tail = take(static_cast<size_t>(S) * 16 * HCA_HEAD_DIM * 2);
@@ -337,14 +345,8 @@ hca_status_t hca_paged_prefill(const hca_bf16* q, const hca_bf16* g, const hca_b
   uint16_t* raw_k = reinterpret_cast<uint16_t*>(w + L.raw_k);
   uint16_t* raw_v = reinterpret_cast<uint16_t*>(w + L.raw_v);
   G::Queries qr = {};
-  qr.count = reinterpret_cast<int*>(w + L.count);
-  if (L.split) {
-    qr.len = reinterpret_cast<int*>(w + L.len);
-    qr.row_of = reinterpret_cast<int*>(w + L.row_of);
-    qr.win_row = reinterpret_cast<int*>(w + L.win_row);
-    qr.gsync = reinterpret_cast<unsigned long long*>(w + L.decode);
-    qr.arrived = reinterpret_cast<unsigned*>(w + L.decode + 256);
-  } else {
+  if (!L.split) {
+    qr.count = reinterpret_cast<int*>(w + L.count);
     qr.items = reinterpret_cast<int4*>(w + L.list);
     qr.cap = L.items;
     qr.tail16 = reinterpret_cast<int*>(w + L.tail16);
@@ -359,32 +361,30 @@ hca_status_t hca_paged_prefill(const hca_bf16* q, const hca_bf16* g, const hca_b
     return paged_items(c, L, w, q, g, out, S, N, scale, vha_down, vha_up, vha_rank,
                        paged_clusters(L.items), stream);
   hca::pdecode::Params prm = {};
-  prm.ctx_len = qr.len;
+  prm.chunk = ch;
+  prm.only_window = 1;
   prm.S = N;
   prm.scale_log2 = scale * 1.4426950408889634f;
   prm.vha_down = vha_down;
   prm.vha_up = vha_up;
   prm.vha_rank = vha_rank;
-  prm.row_of = qr.row_of;
-  prm.win_row = qr.win_row;
-  prm.count = qr.count;
   return paged_attend(c, q, g, out, raw_k, raw_v,
                       static_cast<uint64_t>(N) + static_cast<uint64_t>(G::kPad) * S, prm,
-                      w + L.decode, stream);
+                      w, stream);
 }
 
 size_t hca_paged_decode_workspace_size(int S) {
   if (S < 1) return 0;
   const int sms = device_sms();
   if (sms <= 0) return 0;
-  // grid barrier, counters of the queries, split partials, tile prefix
-  return 256 + align256(static_cast<size_t>(S) * 4) + align256(hca::pdecode::ws_bytes(sms + S)) + static_cast<size_t>(S + 2) * 8;
+  // head, split partials, tile prefix
+  return kHeadBytes + align256(hca::pdecode::ws_bytes(sms + S)) + static_cast<size_t>(S + 2) * 8;
 }
 
 }  // extern "C"
 
 namespace {
-// hca_paged_decode; `step`: behind the append of its tokens, which did not write ctx_len
+// hca_paged_decode; `step`: behind the append of its tokens
 hca_status_t paged_decode(const hca_bf16* q, const hca_bf16* g, const int32_t* ctx_len, int S,
                           int H, float scale, const hca_bf16* vha_down, const hca_bf16* vha_up,
                           int vha_rank, const hca_paged_cache_t* cache, hca_bf16* out, void* ws,
@@ -404,7 +404,7 @@ hca_status_t paged_decode(const hca_bf16* q, const hca_bf16* g, const int32_t* c
   prm.vha_down = vha_down;
   prm.vha_up = vha_up;
   prm.vha_rank = vha_rank;
-  prm.plan_early = step ? 1 : 0;
+  prm.only_window = step && S <= hca::pdecode::kInlineSeqs ? 1 : 0;
   return paged_attend(c, q, g, out, c.wk, c.wv, static_cast<uint64_t>(S) * HCA_WINDOW, prm,
                       static_cast<uint8_t*>(ws), stream);
 }

@@ -400,7 +400,8 @@ size_t hca_paged_prefill_workspace_size(int S, int N);
  *          q_start[S] on are not written.  vha_down, vha_up [64, vha_rank]
  *          bf16 (vha_rank = 0: none, may be NULL).  ws: at least
  *          hca_paged_prefill_workspace_size(S, N) bytes, 256-byte aligned,
- *          needs no initialisation; calls that overlap need one each.
+ *          zero-filled before its first use (every call leaves it valid for
+ *          the next, whatever its S and N); calls that overlap need one each.
  *          A token's values must be finite: one that is not may also reach the
  *          outputs of up to 16 positions before it in its sequence, and
  *          nothing else's.
