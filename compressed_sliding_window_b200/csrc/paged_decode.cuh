@@ -58,6 +58,7 @@ constexpr int kThreads = 32 * (kProducers + 1 + kSoftWarps);
 constexpr int kWarps = kThreads / 32;
 constexpr int kInlineSeqs = 512;    // up to this many queries each CTA plans for itself
 constexpr int kWholeTiles = 3;
+constexpr int kFewSplits = 16;
 constexpr float kTau = 8.0f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -257,14 +258,6 @@ __device__ __forceinline__ void clear_rows(uint8_t* stage, int valid, int lane) 
   }
 }
 
-// One lane of a converged warp, the same one every time.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}" : "=r"(r));
-  return r != 0;
-}
-
 template <int N>
 __device__ __forceinline__ void load_row(const float* src, float (&dst)[N]) {
 #pragma unroll
@@ -393,28 +386,33 @@ __device__ __forceinline__ void merge_query(const Params& p, int s, int c0, int 
     // m and l of every split: head 2 lane, 2 lane + 1
     const float2* ml = reinterpret_cast<const float2*>(p.ws_ml + static_cast<size_t>(c0 + s) * 128);
     float2 M = make_float2(-INFINITY, -INFINITY), L = make_float2(0.f, 0.f);
-    if (n <= 4) {   // few splits: every warp for itself, without barriers
-      float2 m[4], l[4];
+    if (n <= kFewSplits) {   // every warp for itself, without barriers
+      float2* w = reinterpret_cast<float2*>(wt) + warp * kFewSplits * 32;
+      wt = reinterpret_cast<float*>(w);
+      add = reinterpret_cast<float*>(smem + kSmemRing);
+      float2 m[kFewSplits], l[kFewSplits];
 #pragma unroll
-      for (int f = 0; f < 4; ++f) {
+      for (int f = 0; f < kFewSplits; ++f) {
         m[f] = f < n ? __ldcg(ml + 64 * f + lane) : make_float2(-INFINITY, -INFINITY);
         l[f] = f < n ? __ldcg(ml + 64 * f + 32 + lane) : make_float2(0.f, 0.f);
+      }
+#pragma unroll
+      for (int f = 0; f < kFewSplits; ++f) {
         M.x = fmaxf(M.x, m[f].x);
         M.y = fmaxf(M.y, m[f].y);
       }
 #pragma unroll
-      for (int f = 0; f < 4; ++f) {
+      for (int f = 0; f < kFewSplits; ++f) {
         l[f].x *= ex2_approx(m[f].x - M.x);
         l[f].y *= ex2_approx(m[f].y - M.y);
         L.x += l[f].x;
         L.y += l[f].y;
       }
-      float2* w = reinterpret_cast<float2*>(wt) + warp * 4 * 32;
-      wt = reinterpret_cast<float*>(w);
-      add = reinterpret_cast<float*>(smem + kSmemRing);
+      L.x = 1.f / L.x;
+      L.y = 1.f / L.y;
 #pragma unroll
-      for (int f = 0; f < 4; ++f)
-        w[32 * f + lane] = make_float2(l[f].x / L.x, l[f].y / L.y);
+      for (int f = 0; f < kFewSplits; ++f)
+        if (f < n) w[32 * f + lane] = make_float2(l[f].x * L.x, l[f].y * L.y);
       __syncwarp();
     } else {
       float2* w = reinterpret_cast<float2*>(wt);

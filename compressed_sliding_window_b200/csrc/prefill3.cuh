@@ -360,6 +360,16 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
   if constexpr (kPaged) asm volatile("griddepcontrol.wait;" ::: "memory");
   const int items = kPaged ? *p.item_count : p.items;
   const uint32_t tmem = *tmem_slot;
+  // warp-collective waits of the MMA warps, and the TMEM base in a uniform register
+  const uint32_t utmem = __shfl_sync(0xffffffffu, tmem, 0);
+  auto wait_cta = [&](uint32_t b, uint32_t parity, unsigned where) -> bool {
+    return __all_sync(0xffffffffu, mbar_try_wait(b, parity)) ||
+           mbar_wait_warp(b, parity, abort_flag, kWaitLimitNs, where);
+  };
+  auto wait_cluster = [&](uint32_t b, uint32_t parity, unsigned where) -> bool {
+    return __all_sync(0xffffffffu, mbar_try_wait_acq_cluster(b, parity)) ||
+           mbar_wait_cluster_warp(b, parity, abort_flag, kWaitLimitNs, where);
+  };
 
   if (!isO) {
     // =====================================================================
@@ -475,45 +485,44 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 2) {
       // --------------------------------------------------------- MMA (S = Q K^T), even CTA
-      if (leader && lane == 0) {
+      // (the whole warp waits, one elected lane issues)
+      if (leader) {
         uint32_t u = 0, sj = 0, nitem = 0;
         bool ok = true;
         for (int it = cluster; it < items && ok; it += nclusters, ++nitem) {
           const Item x = decode_item<kPaged>(p, it);
           for (int j = 0; j < x.ntiles && ok; ++j, ++sj) {
             const uint32_t buf = sj & 1;
-            ok &= mbar_wait_cluster(bar(SFREE + buf), ((sj >> 1) & 1) ^ 1, abort_flag,
-                                    kWaitLimitNs, 320);
+            ok &= wait_cluster(bar(SFREE + buf), ((sj >> 1) & 1) ^ 1, 320);
             const uint32_t idesc =
                 idesc_bf16_f32(2 * kRows, tile_s<kPaged>(p, x, j), false, false);
-            const uint32_t dS = tmem + 256 * buf;
+            const uint32_t dS = utmem + 256 * buf;
             const bool first = j == 0, last = j + 1 == x.ntiles;
 #pragma unroll 1
             for (int d2 = 0; d2 < 4; ++d2, ++u) {
-              if (first && (d2 & 1) == 0)
-                ok &= mbar_wait(bar(QFULL + (d2 >> 1)), nitem & 1, abort_flag, kWaitLimitNs, 321);
+              if (first && (d2 & 1) == 0) ok &= wait_cta(bar(QFULL + (d2 >> 1)), nitem & 1, 321);
               const uint32_t st = u % kKStages;
-              ok &= mbar_wait(bar(KFULL + st), (u / kKStages) & 1, abort_flag, kWaitLimitNs, 322);
+              ok &= wait_cta(bar(KFULL + st), (u / kKStages) & 1, 322);
               tc_fence_after();
-              const uint32_t ka = sb + S_KRING + st * kKStage;
+              const uint64_t kd = sdesc_sw128(sb + S_KRING + st * kKStage, 16, 1024);
+              const uint64_t qd = sdesc_sw128(sb + S_Q + d2 * 32768, 16, 1024);
+              if (elect_one()) {
 #pragma unroll
-              for (int s = 0; s < 2; ++s) {
-                const int d = 2 * d2 + s;
-                const uint32_t qa = sb + S_Q + (d >> 2) * kQHalf + (d & 3) * 16384;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  umma_pair_if(dS, sdesc_sw128(qa + 32 * k, 16, 1024),
-                               sdesc_sw128(ka + s * kKSlab + 32 * k, 16, 1024), idesc,
-                               (d | k) != 0, true);
+                for (int k = 0; k < 8; ++k) {   // 16 channels each: 32 bytes on, or the next slab
+                  const uint32_t o = 2 * (k & 3) + (k >> 2) * (kKSlab >> 4);
+                  umma_pair_if(dS, qd + o, kd + o, idesc, (d2 | k) != 0, true);
+                }
+                umma_pair_commit_mc(bar(KEMPTY + st), kMaskS);
+                if (last && (d2 & 1) == 1) umma_pair_commit_mc(bar(QEMPTY + (d2 >> 1)), kMaskS);
+                if (d2 == 3) umma_pair_commit_mc(bar(SFULL + buf), kMaskS);
               }
-              umma_pair_commit_mc(bar(KEMPTY + st), kMaskS);
-              umma_pair_commit_mc_if(bar(QEMPTY + (d2 >> 1)), kMaskS, last && (d2 & 1) == 1);
+              __syncwarp();
             }
-            umma_pair_commit_mc(bar(SFULL + buf), kMaskS);
           }
         }
-        umma_pair_commit_mc(bar(DRAIN), 1u << rank);
-        mbar_wait(bar(DRAIN), 0, abort_flag, kWaitLimitNs, 323);
+        if (elect_one()) umma_pair_commit_mc(bar(DRAIN), 1u << rank);
+        __syncwarp();
+        wait_cta(bar(DRAIN), 0, 323);
       }
     } else if (warp >= 11) {
       // the P copier, store and helper roles exist on O-CTAs only
@@ -923,7 +932,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 2) {
       // --------------------------------------------------------- MMA (O += P V), even CTA
-      if (leader && lane == 0) {
+      // (the whole warp waits, one elected lane issues)
+      if (leader) {
         uint32_t u = 0, sj = 0, nitem = 0, ncorr = 0, vpar = 0;
         bool ok = true;
         const uint32_t idesc = idesc_bf16_f32(2 * kRows, 256, false, true);
@@ -939,20 +949,22 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             const uint64_t bm = sdesc_sw128(sb + O_VHAB + 4096, 16, 1024);
 #pragma unroll 1
             for (int e = e0; e < e1; ++e) {
-              if (!mbar_wait_cluster(bar(XSTAGED + e), par, abort_flag, kWaitLimitNs, 355))
-                return false;
+              if (!wait_cluster(bar(XSTAGED + e), par, 355)) return false;
               tc_fence_after();
               const uint32_t st = (gb + e) % NV;
+              if (elect_one()) {
 #pragma unroll
               for (int pp = 0; pp < 2; ++pp) {
                 const uint64_t ad =
                     sdesc_sw128(sb + O_VRING + st * kVStage + 8192 * pp, 16384, 1024);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                  umma_pair_if(tmem + 128 * e + 64 * pp, ad + 128 * (k & 3),
+                  umma_pair_if(utmem + 128 * e + 64 * pp, ad + 128 * (k & 3),
                                (k < 4 ? bi : bm) + 2 * (k & 3), vdesc, k == 0 ? 0u : 1u, true);
               }
               umma_pair_commit_mc(bar(VHADONE + e), kMaskO);
+              }
+              __syncwarp();
             }
           }
           return true;
@@ -964,7 +976,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t vha_gb = 0, vha_par = 0;
         auto vha_poll = [&](bool block) -> bool {
           while (vha_next < 4) {
-            if (!block && !mbar_try_wait_acq_cluster(bar(XSTAGED + vha_next), vha_par)) return true;
+            if (!block &&
+                !__all_sync(0xffffffffu, mbar_try_wait_acq_cluster(bar(XSTAGED + vha_next), vha_par)))
+              return true;
             if (!vha_issue(vha_next, vha_next + 1, vha_gb, vha_par)) return false;
             ++vha_next;
           }
@@ -975,8 +989,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
           for (int j = 0; j < x.ntiles && ok; ++j, ++sj) {
             const int n = tile_n(x, j);
             if (j > 0)  // an item's first tile never needs a rescale of O
-              ok &= mbar_wait_cluster(bar(CORR + (ncorr & 1)), (ncorr >> 1) & 1, abort_flag,
-                                      kWaitLimitNs, 351);
+              ok &= wait_cluster(bar(CORR + (ncorr & 1)), (ncorr >> 1) & 1, 351);
             ncorr += (j > 0);
             const bool first = j == 0, last = j == x.ntiles - 1;
             const int nh1 = sub_n(n, 1);
@@ -989,43 +1002,56 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
               pv_stage(s, two, first || last, dh, h);
               if (kVha && vha_next < 4) ok &= vha_poll(first && dh == 1);
               if (first && h == 0)  // this value half of the last item's O is read out
-                ok &= mbar_wait_cluster(bar(OFREE + dh), (nitem & 1) ^ 1, abort_flag, kWaitLimitNs,
-                                        352);
-              if (dh == 0) ok &= mbar_wait(bar(PFULL + h), sj & 1, abort_flag, kWaitLimitNs, 350);
+                ok &= wait_cluster(bar(OFREE + dh), (nitem & 1) ^ 1, 352);
+              if (dh == 0) ok &= wait_cta(bar(PFULL + h), sj & 1, 350);
               const uint32_t st = u % NV;
-              ok &= mbar_wait(bar(VFULL + st), (vpar >> st) & 1, abort_flag, kWaitLimitNs, 353);
+              ok &= wait_cta(bar(VFULL + st), (vpar >> st) & 1, 353);
               vpar ^= 1u << st;
               tc_fence_after();
               // eight K steps of 16 keys; descriptors move by their start address
               const int ksteps = sub_n(n, h) >> 4;
               const uint64_t ad = sdesc_noswz(sb + O_P + h * kPBuf, 2048, 128);
               const uint64_t bd = sdesc_sw128(sb + O_VRING + st * kVStage, 16384, 1024);
-              const uint32_t dt = tmem + 256 * dh;
+              const uint32_t dt = utmem + 256 * dh;
               const uint32_t acc0 = (first && h == 0) ? 0u : 1u;
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                umma_pair_if(dt, ad + 256 * k, bd + 128 * k, idesc, k == 0 ? acc0 : 1u, k < ksteps);
-              umma_pair_commit_mc(bar(VEMPTY + st), kMaskO);
               // P buffer h done once value half 1 used it; O half 0 final after
               // the last tile's half-0 stages
               const bool pdone = dh == 1;
               const bool o0 = last && dh == 0 && h == (two ? 1 : 0);
-              if (pdone || o0) {
-                umma_pair_commit_mc_if(bar(PBUFFREE + h), kMaskO, pdone);  // smem P buffers
-                umma_pair_commit_mc_if(pfree0 + 8 * h, kMaskS, pdone);     // scratch slots
-                umma_pair_commit_mc_if(bar(OFULL + 0), kMaskO, o0);
+              if (elect_one()) {
+                if (ksteps == 8) {
+#pragma unroll
+                  for (int k = 0; k < 8; ++k)
+                    umma_pair_if(dt, ad + 256 * k, bd + 128 * k, idesc, k == 0 ? acc0 : 1u, true);
+                } else {
+#pragma unroll 1
+                  for (int k = 0; k < ksteps; ++k)
+                    umma_pair_if(dt, ad + 256 * k, bd + 128 * k, idesc, k == 0 ? acc0 : 1u, true);
+                }
+                umma_pair_commit_mc(bar(VEMPTY + st), kMaskO);
+                if (pdone) {
+                  umma_pair_commit_mc(bar(PBUFFREE + h), kMaskO);   // smem P buffers
+                  umma_pair_commit_mc(pfree0 + 8 * h, kMaskS);      // scratch slots
+                }
+                if (o0) umma_pair_commit_mc(bar(OFULL + 0), kMaskO);
               }
+              __syncwarp();
             }
             if (!two) {  // empty sub-tile 1: its buffer handshake still runs
-              ok &= mbar_wait(bar(PFULL + 1), sj & 1, abort_flag, kWaitLimitNs, 350);
+              ok &= wait_cta(bar(PFULL + 1), sj & 1, 350);
               tc_fence_after();
-              umma_pair_commit_mc(bar(PBUFFREE + 1), kMaskO);
-              umma_pair_commit_mc(pfree0 + 8, kMaskS);
             }
-            umma_pair_commit_mc(bar(PVDONE + (sj & 1)), kMaskO);   // all of tile sj's P.V
+            if (elect_one()) {
+              if (!two) {
+                umma_pair_commit_mc(bar(PBUFFREE + 1), kMaskO);
+                umma_pair_commit_mc(pfree0 + 8, kMaskS);
+              }
+              umma_pair_commit_mc(bar(PVDONE + (sj & 1)), kMaskO);   // all of tile sj's P.V
+              if (last) umma_pair_commit_mc(bar(OFULL + 1), kMaskO);
+            }
+            __syncwarp();
           }
           if (!ok) break;
-          umma_pair_commit_mc(bar(OFULL + 1), kMaskO);
           if constexpr (kVha) {
             ok = vha_issue(0, 2, u, nitem & 1);   // value half 0 now, half 1 polled
             if (!ok) break;
@@ -1036,8 +1062,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
           u += 4;  // gate stages, consumed by the epilogue
         }
         if (kVha && ok) ok = vha_poll(true);
-        umma_pair_commit_mc(bar(DRAIN), 1u << rank);
-        mbar_wait(bar(DRAIN), 0, abort_flag, kWaitLimitNs, 354);
+        if (elect_one()) umma_pair_commit_mc(bar(DRAIN), 1u << rank);
+        __syncwarp();
+        wait_cta(bar(DRAIN), 0, 354);
       }
     } else if (warp >= 3) {
       // --------------------------------------------------------- correction + epilogue
