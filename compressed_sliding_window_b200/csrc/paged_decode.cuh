@@ -58,7 +58,6 @@ constexpr int kThreads = 32 * (kProducers + 1 + kSoftWarps);
 constexpr int kWarps = kThreads / 32;
 constexpr int kInlineSeqs = 512;    // up to this many queries each CTA plans for itself
 constexpr int kWholeTiles = 3;
-constexpr int kFewSplits = 16;
 constexpr float kTau = 8.0f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -81,7 +80,7 @@ static_assert(kStages * kStage == kKeyTile * kDim * 2, "a tile's K or V is one r
 enum {
   B_QFULL = 0, B_QEMPTY = 1, B_FULL = 2, B_EMPTY = B_FULL + kStages, B_SFULL = B_EMPTY + kStages,
   B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2, B_PFREE = B_PFULL + 1, B_OFULL = B_PFREE + 1,
-  B_OFREE = B_OFULL + 1, B_DRAIN = B_OFREE + 1, B_COUNT = B_DRAIN + 1
+  B_OFREE = B_OFULL + 1, B_DRAIN = B_OFREE + 1, B_MERGE = B_DRAIN + 1, B_COUNT = B_MERGE + 1
 };
 constexpr int kTmemSlot = 8 * B_COUNT;
 constexpr int kAbortSlot = kTmemSlot + 4;
@@ -350,17 +349,43 @@ __device__ __forceinline__ void own_query(const long long* tiles, int S, int lon
 // takes the chunks (16 heads x 32 value columns) [64 i / n, 64 (i + 1) / n) of
 // all n partials, once all have been written (a counter per query; a CTA waits
 // only for those that share its first or last query, and only after its own
-// tiles).  The weights w = l_f 2^(m_f - M) / L of all splits and heads are found
-// in shared memory first; then a warp adds up a chunk, lane l holding heads
-// 4 q + l / 8 and columns 4 (l % 8) .. + 3 (a chunk of a split is four 16-byte
-// loads a lane, four splits in flight).  With fewer chunks than warps, several
+// tiles).  A split's share is contiguous, so one bulk copy brings it into shared
+// memory (a CTA's own stays there from the start where its tiles are one part
+// of one query); meanwhile the warps find the weights w = l_f 2^(m_f - M) / L of
+// all splits and heads.  Then a warp adds up a chunk, lane l holding heads
+// 4 q + l / 8 and columns 4 (l % 8) .. + 3.  With fewer chunks than warps, several
 // warps share a chunk's splits and add up through shared memory.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void merge_query(const Params& p, int s, int c0, int n, uint8_t* smem,
-                                            int warp, int lane) {
+// Splits up to which the weights fit the P^T buffer; with more the Q buffer
+// takes them, and the data have the ring alone.
+constexpr int kFewSplits = 64;
+__device__ __forceinline__ int merge_room(int n) { return n <= kFewSplits ? 96 : 64; }   // chunks
+__device__ __forceinline__ uint32_t merge_data(int n) { return n <= kFewSplits ? kSmemQ : kSmemRing; }
+// first chunk and number of chunks of CTA i of n
+__device__ __forceinline__ int merge_first(int i, int n) { return 64 * i / n; }
+
+__device__ __forceinline__ void merge_query(const Params& p, int s, int c0, int n, bool kept,
+                                            uint8_t* smem, uint32_t sbase, uint32_t bar_m,
+                                            uint32_t& phase, volatile int* abort_flag, int warp,
+                                            int lane) {
   const int i = static_cast<int>(blockIdx.x) - c0;
-  const int k0 = 64 * i / n, nk = 64 * (i + 1) / n - k0;
+  const int k0 = merge_first(i, n), nk = merge_first(i + 1, n) - k0;
+  const int batch = nk > 0 ? min(n, merge_room(n) / nk) : n;   // splits at a time
+  const uint32_t data = merge_data(n);
+  const float* po = p.ws_o + static_cast<size_t>(c0 + s) * kHeads * kDim + 512 * k0;
   __shared__ int late;
+  auto load = [&](int f0, int f1) {   // one thread
+    uint32_t bytes = 0;
+    for (int f = f0; f < f1; ++f) bytes += (kept && f == i) ? 0u : 2048u * nk;
+    mbar_expect_tx(bar_m, bytes);
+    for (int f = f0; f < f1; ++f)
+      if (!(kept && f == i))
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1], %2, [%3];" ::"r"(sbase + data + 2048u * nk * (f - f0)),
+            "l"(po + static_cast<size_t>(f) * kHeads * kDim), "r"(2048u * nk), "r"(bar_m)
+            : "memory");
+  };
   if (threadIdx.x == 0) {
     const uint64_t t0 = globaltimer_ns();
     late = 0;
@@ -374,76 +399,55 @@ __device__ __forceinline__ void merge_query(const Params& p, int s, int c0, int 
         break;
       }
     }
-    fence_proxy_async_all();   // the partials were written by bulk copies
+    if (nk > 0 && !late) {
+      fence_proxy_async_all();   // read by bulk copies; and this memory's earlier generic uses
+      load(0, batch);
+    }
   }
   __syncthreads();
   if (nk > 0 && !late) {
+    // heads 2 lane, 2 lane + 1: M and L over the splits, every warp for itself, then the
+    // weights of splits warp, warp + kWarps, ..
+    const float2* ml = reinterpret_cast<const float2*>(p.ws_ml + static_cast<size_t>(c0 + s) * 128);
+    float* w = reinterpret_cast<float*>(smem + (n <= kFewSplits ? kSmemPT : kSmemQ));   // [n][64]
+    float2 M = make_float2(-INFINITY, -INFINITY), L = make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (int f0 = 0; f0 < n; f0 += 8) {
+      float2 m[8], l[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const bool in = f0 + u < n;
+        m[u] = in ? __ldcg(ml + 64 * (f0 + u) + lane) : make_float2(-INFINITY, -INFINITY);
+        l[u] = in ? __ldcg(ml + 64 * (f0 + u) + 32 + lane) : make_float2(0.f, 0.f);
+      }
+      float2 T = M;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        T.x = fmaxf(T.x, m[u].x);
+        T.y = fmaxf(T.y, m[u].y);
+      }
+      L.x *= ex2_approx(M.x - T.x);   // the first time 0 x 2^-inf
+      L.y *= ex2_approx(M.y - T.y);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        L.x = fmaf(l[u].x, ex2_approx(m[u].x - T.x), L.x);
+        L.y = fmaf(l[u].y, ex2_approx(m[u].y - T.y), L.y);
+      }
+      M = T;
+    }
+    const float2 inv = make_float2(1.f / L.x, 1.f / L.y);
+    for (int f = warp; f < n; f += kWarps) {
+      const float2 m = __ldcg(ml + 64 * f + lane), l = __ldcg(ml + 64 * f + 32 + lane);
+      *reinterpret_cast<float2*>(w + 64 * f + 2 * lane) =
+          make_float2(l.x * ex2_approx(m.x - M.x) * inv.x, l.y * ex2_approx(m.y - M.y) * inv.y);
+    }
+    __syncthreads();
     const int share = nk < kWarps ? kWarps / nk : 1;            // warps per chunk
     const int part = warp % share, slot0 = warp / share, chunks = kWarps / share;
-    const float* po = p.ws_o + static_cast<size_t>(c0 + s) * kHeads * kDim + 4 * lane;
-    float* wt = reinterpret_cast<float*>(smem + kSmemQ);        // [n][64] m, then weights
-    float* add = wt + static_cast<size_t>(n) * kHeads;          // [warps][512]
-    // m and l of every split: head 2 lane, 2 lane + 1
-    const float2* ml = reinterpret_cast<const float2*>(p.ws_ml + static_cast<size_t>(c0 + s) * 128);
-    float2 M = make_float2(-INFINITY, -INFINITY), L = make_float2(0.f, 0.f);
-    if (n <= kFewSplits) {   // every warp for itself, without barriers
-      float2* w = reinterpret_cast<float2*>(wt) + warp * kFewSplits * 32;
-      wt = reinterpret_cast<float*>(w);
-      add = reinterpret_cast<float*>(smem + kSmemRing);
-      float2 m[kFewSplits], l[kFewSplits];
-#pragma unroll
-      for (int f = 0; f < kFewSplits; ++f) {
-        m[f] = f < n ? __ldcg(ml + 64 * f + lane) : make_float2(-INFINITY, -INFINITY);
-        l[f] = f < n ? __ldcg(ml + 64 * f + 32 + lane) : make_float2(0.f, 0.f);
-      }
-#pragma unroll
-      for (int f = 0; f < kFewSplits; ++f) {
-        M.x = fmaxf(M.x, m[f].x);
-        M.y = fmaxf(M.y, m[f].y);
-      }
-#pragma unroll
-      for (int f = 0; f < kFewSplits; ++f) {
-        l[f].x *= ex2_approx(m[f].x - M.x);
-        l[f].y *= ex2_approx(m[f].y - M.y);
-        L.x += l[f].x;
-        L.y += l[f].y;
-      }
-      L.x = 1.f / L.x;
-      L.y = 1.f / L.y;
-#pragma unroll
-      for (int f = 0; f < kFewSplits; ++f)
-        if (f < n) w[32 * f + lane] = make_float2(l[f].x * L.x, l[f].y * L.y);
-      __syncwarp();
-    } else {
-      float2* w = reinterpret_cast<float2*>(wt);
-      for (int f = warp; f < n; f += kWarps) w[32 * f + lane] = __ldcg(ml + 64 * f + lane);
-      __syncthreads();
-      for (int f = 0; f < n; ++f) {
-        const float2 m = w[32 * f + lane];
-        M.x = fmaxf(M.x, m.x);
-        M.y = fmaxf(M.y, m.y);
-      }
-      __syncthreads();
-      for (int f = warp; f < n; f += kWarps) {
-        const float2 m = w[32 * f + lane], l = __ldcg(ml + 64 * f + 32 + lane);
-        w[32 * f + lane] = make_float2(l.x * ex2_approx(m.x - M.x), l.y * ex2_approx(m.y - M.y));
-      }
-      __syncthreads();
-      for (int f = 0; f < n; ++f) {
-        const float2 x = w[32 * f + lane];
-        L.x += x.x;
-        L.y += x.y;
-      }
-      __syncthreads();
-      for (int f = warp; f < n; f += kWarps) {
-        const float2 x = w[32 * f + lane];
-        w[32 * f + lane] = make_float2(x.x / L.x, x.y / L.y);
-      }
-      __syncthreads();
-    }
+    // More than one batch only where nk <= 2 (and so one round of chunks).
     for (int r0 = 0; r0 < nk; r0 += chunks) {
-      const int k = k0 + r0 + slot0;
-      const bool mine = slot0 < chunks && r0 + slot0 < nk;
+      const int r = r0 + slot0, k = k0 + r;
+      const bool mine = slot0 < chunks && r < nk;
       const int h0 = 16 * (k >> 4) + (lane >> 3);               // heads h0 + 4 q
       const size_t at = (static_cast<size_t>(s) * kHeads + h0) * kDim + 32 * (k & 15) + 4 * (lane & 7);
       float acc[16];
@@ -454,33 +458,40 @@ __device__ __forceinline__ void merge_query(const Params& p, int s, int c0, int 
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           gv[q] = __ldg(reinterpret_cast<const uint2*>(p.g + at + 4 * q * kDim));
-#pragma unroll 1
-        for (int f0 = part; f0 < n; f0 += 4 * share) {
-          float4 x[4][4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int f = f0 + u * share;
-            const float4* src = reinterpret_cast<const float4*>(
-                po + static_cast<size_t>(f) * kHeads * kDim + 512 * k);
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              x[u][q] = f < n ? __ldcg(src + 32 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      for (int f0 = 0; f0 < n; f0 += batch) {
+        const int f1 = min(n, f0 + batch);
+        if (f0 > 0) {
+          __syncthreads();   // the last batch has been read
+          if (threadIdx.x == 0) {
+            fence_proxy_async_all();
+            load(f0, f1);
           }
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int f = f0 + u * share;
+        }
+        if (r0 == 0) {
+          // late copies may still land: nobody may leave before abort_drain
+          if (!mbar_wait_warp(bar_m, phase, abort_flag, kWaitLimitNs, 73) && lane == 0)
+            abort_drain(abort_flag);
+          phase ^= 1;
+        }
+        if (mine) {
+          const float4* src = reinterpret_cast<const float4*>(smem + data) + 128 * r + lane;
+#pragma unroll 2
+          for (int f = f0 + part; f < f1; f += share) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const float wf = f < n ? wt[64 * f + h0 + 4 * q] : 0.f;
-              acc[4 * q] = fmaf(wf, x[u][q].x, acc[4 * q]);
-              acc[4 * q + 1] = fmaf(wf, x[u][q].y, acc[4 * q + 1]);
-              acc[4 * q + 2] = fmaf(wf, x[u][q].z, acc[4 * q + 2]);
-              acc[4 * q + 3] = fmaf(wf, x[u][q].w, acc[4 * q + 3]);
+              const float4 x = src[128 * nk * (f - f0) + 32 * q];
+              const float wf = w[64 * f + h0 + 4 * q];
+              acc[4 * q] = fmaf(wf, x.x, acc[4 * q]);
+              acc[4 * q + 1] = fmaf(wf, x.y, acc[4 * q + 1]);
+              acc[4 * q + 2] = fmaf(wf, x.z, acc[4 * q + 2]);
+              acc[4 * q + 3] = fmaf(wf, x.w, acc[4 * q + 3]);
             }
           }
         }
       }
-      if (share > 1) {   // uniform in the CTA
+      if (share > 1) {   // uniform in the CTA; the data have been read by all
+        float* add = reinterpret_cast<float*>(smem + data);       // [warps][512]
         __syncthreads();
         if (mine && part > 0) {
 #pragma unroll
@@ -559,6 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(B_OFULL), 1);
     mbar_init(bar(B_OFREE), kSoftWarps);
     mbar_init(bar(B_DRAIN), 1);
+    mbar_init(bar(B_MERGE), 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&maps.q);
@@ -615,6 +627,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     A0 = decode::div_nn(N * cta, G);
     A1 = decode::div_nn(N * (cta + 1), G);
   }
+  // own: this CTA's share of its own partial stays in shared memory, where nothing
+  // follows its only segment, if all splits' shares fit there at once
+  const int k0 = own && parts > 1 ? merge_first(part, parts) : 0;
+  const int nk = own && parts > 1 ? merge_first(part + 1, parts) - k0 : 0;
+  const bool kept = nk > 0 && parts * nk <= merge_room(parts);
   auto owner = [&](long long x) -> int {   // even cut: CTA of tile x
     return static_cast<int>(decode::div_nn((x + 1) * G + N - 1, N)) - 1;
   };
@@ -1050,7 +1067,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok) ok = mbar_wait_warp(bar(B_OFULL), nseg & 1, abort_flag, kWaitLimitNs, 62);
         tc_fence_after();
-        float* wo = p.ws_o + slot * kHeads * kDim + (2 * half * 16 + wq) * 512;
+        float* wo = p.ws_o + slot * kHeads * kDim + lane;
+        float* keep = reinterpret_cast<float*>(smem + merge_data(parts)) + 512 * nk * part + lane;
+        auto chunk_at = [&](int k) -> float* {
+          return kept && k >= k0 && k < k0 + nk ? keep + 512 * (k - k0) : wo + 512 * k;
+        };
         float inv[32];
         load_row<32>(mrow + 32, inv);      // before the stores, which it could not pass
 #pragma unroll 1
@@ -1060,12 +1081,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(tl + kTmemO + 128 * i + 64, o + 32);
           tmem_wait_ld_dep32(o);
           reg_dep32(o + 32);
-          float* dst = wo + 8 * i * 512 + lane;
 #pragma unroll
-          for (int h = 0; h < 32; ++h) {
-            dst[(h >> 4) * 16 * 512 + 32 * (h & 15)] = __uint_as_float(o[h]) * inv[h];
-            dst[(h >> 4) * 16 * 512 + 4 * 512 + 32 * (h & 15)] = __uint_as_float(o[32 + h]) * inv[h];
-          }
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int hb = 0; hb < 2; ++hb) {
+              float* dst = chunk_at(16 * (2 * half + hb) + 4 * (2 * i + c) + wq);
+#pragma unroll
+              for (int h = 0; h < 16; ++h)
+                dst[32 * h] = __uint_as_float(o[32 * c + 16 * hb + h]) * inv[16 * hb + h];
+            }
         }
         // the partial is written: one arrival for the CTAs that share the query
         named_bar_sync(3, 32 * kSoftWarps);
@@ -1129,14 +1153,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
   };
+  uint32_t merges = 0;   // phase of B_MERGE
   if (own) {
-    if (parts > 1) merge_query(p, mine, cta - part, parts, smem, warp, lane);
+    if (parts > 1)
+      merge_query(p, mine, cta - part, parts, kept, smem, sbase, bar(B_MERGE), merges, abort_flag,
+                  warp, lane);
   } else if (!whole && A0 < A1) {
     // the first and the last query of this CTA may be shared with others
     const int sa = find_seq(tiles, p.S, A0), sb = find_seq(tiles, p.S, A1 - 1);
     for (int s = sa; s <= sb; s += max(sb - sa, 1)) {
       const int c0 = owner(tiles[s]), n = owner(tiles[s + 1] - 1) - c0 + 1;
-      if (n > 1) merge_query(p, s, c0, n, smem, warp, lane);
+      if (n > 1)
+        merge_query(p, s, c0, n, false, smem, sbase, bar(B_MERGE), merges, abort_flag, warp, lane);
     }
   }
   if (p.vha_rank > 0) {
