@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -34,22 +35,10 @@ class HCAError(RuntimeError):
         self.code = code
 
 
-class _PagedCache(ctypes.Structure):      # hca_paged_cache_t
-    _fields_ = [(n, ctypes.c_void_p) for n in ("wk", "wv", "ws", "ck", "cv", "page_table")] + [
-        ("table_stride", ctypes.c_longlong), ("max_pages", ctypes.c_int),
-        ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int)]
-
-
-class _PageTable(ctypes.Structure):       # hca_page_table_t
-    _fields_ = [("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_longlong),
-                ("rows", ctypes.c_int), ("max_pages", ctypes.c_int),
-                ("n_pages", ctypes.c_void_p), ("ref", ctypes.c_void_p),
-                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int)]
-
-
-class _PageArray(ctypes.Structure):       # hca_page_array_t
-    _fields_ = [("data", ctypes.c_void_p), ("item_bytes", ctypes.c_longlong)]
-
+# The C structures of hca.h, native alignment (their pointers are read during the call only)
+_PAGED_CACHE = struct.Struct("@6Pqiii4x").pack      # hca_paged_cache_t
+_PAGE_TABLE = struct.Struct("@PqiiPPii").pack        # hca_page_table_t
+_PAGE_ARRAY = struct.Struct("@Pq").pack              # hca_page_array_t
 
 _LIB = None
 
@@ -84,7 +73,7 @@ def lib() -> ctypes.CDLL:
         L.hca_quantize_e4m3.argtypes = [vp, ctypes.c_longlong, vp, vp, vp]
         L.hca_decode_e4m3.argtypes = [vp, vp, vp, vp, vp, i, vp, vp, vp, vp, vp, vp, i, i, f, vp,
                                       sz, vp, vp]
-        pc, pt, pa = (ctypes.POINTER(t) for t in (_PagedCache, _PageTable, _PageArray))
+        pc = pt = pa = ctypes.c_char_p     # packed structures
         L.hca_paged_append.argtypes = [vp, vp, vp, vp, vp, i, i, pc, vp]
         L.hca_paged_prefill_workspace_size.argtypes = [i, i]
         L.hca_paged_prefill_workspace_size.restype = sz
@@ -442,13 +431,15 @@ PAGE_SIZES = (16, 32, 64, 128)
 _SCALE = 1.0 / math.sqrt(HEAD_DIM)
 
 
-def _need(t: torch.Tensor, name: str, shape, dtype, device):
+def _need(t: torch.Tensor, name: str, shape, dtype, device) -> int:
     """_check, and that t lies on `device`, at the cost of a few attribute reads: a
-    serving step checks a dozen tensors while the GPU waits for its launch."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+    serving step checks a dozen tensors while the GPU waits for its launch.  Returns
+    the data pointer."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
             and t.device == device and t.is_contiguous()):
-        _check(t, name, shape, dtype=dtype)
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+        return t.data_ptr()
+    _check(t, name, shape, dtype=dtype)
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
 def _device_of(t: torch.Tensor, name: str) -> torch.device:
@@ -484,8 +475,8 @@ def _cuda(device) -> torch.device:
 
 
 def _workspace(workspace: torch.Tensor, device):
-    _need(workspace, "workspace", (workspace.numel(),), torch.uint8, device)
-    return workspace.data_ptr(), workspace.numel()
+    n = workspace.numel()
+    return _need(workspace, "workspace", (n,), torch.uint8, device), n
 
 
 def _check_table(page_table: torch.Tensor, rows: int, device):
@@ -502,50 +493,54 @@ def _check_table(page_table: torch.Tensor, rows: int, device):
     return cols, stride
 
 
-def _paged_cache(S, wk, wv, ws, ck_pages, cv_pages, page_table, device) -> _PagedCache:
+def _paged_cache(S, wk, wv, ws, ck_pages, cv_pages, page_table, device) -> bytes:
     bf16 = torch.bfloat16
-    _need(wk, "wk", (S, WINDOW, HEAD_DIM), bf16, device)
-    _need(wv, "wv", (S, WINDOW, HEAD_DIM), bf16, device)
-    if ws is not None:
-        _need(ws, "ws", (S, WINDOW), bf16, device)
+    ring = (S, WINDOW, HEAD_DIM)
+    pk = _need(wk, "wk", ring, bf16, device)
+    pv = _need(wv, "wv", ring, bf16, device)
+    ps = 0 if ws is None else _need(ws, "ws", (S, WINDOW), bf16, device)
     if not isinstance(ck_pages, torch.Tensor) or ck_pages.dim() != 3:
         raise ValueError("ck_pages must be [num_pages, page_size, 512]")
     num, size, _ = ck_pages.shape
     if size not in PAGE_SIZES:
         raise ValueError(f"pages must hold 16, 32, 64 or 128 entries, got {size}")
-    _need(ck_pages, "ck_pages", (num, size, HEAD_DIM), bf16, device)
-    _need(cv_pages, "cv_pages", (num, size, HEAD_DIM), bf16, device)
+    pool = (num, size, HEAD_DIM)
+    pck = _need(ck_pages, "ck_pages", pool, bf16, device)
+    pcv = _need(cv_pages, "cv_pages", pool, bf16, device)
     cols, stride = _check_table(page_table, S, device)
-    return _PagedCache(wk.data_ptr(), wv.data_ptr(), None if ws is None else ws.data_ptr(),
-                       ck_pages.data_ptr() if num else None, cv_pages.data_ptr() if num else None,
-                       page_table.data_ptr() if cols else None, stride, cols, num, size)
+    return _PAGED_CACHE(pk, pv, ps, pck if num else 0, pcv if num else 0,
+                        page_table.data_ptr() if cols else 0, stride, cols, num, size)
 
 
 def _check_chunk(k_new, v_new, s_new, q_start, ctx_len, device):
+    """(pointers of k_new, v_new, s_new, q_start, ctx_len, then S, N)"""
     S = ctx_len.shape[0]
     N = k_new.shape[0]
     bf16 = torch.bfloat16
-    _need(ctx_len, "ctx_len", (S,), torch.int32, device)
-    _need(k_new, "k_new", (N, HEAD_DIM), bf16, device)
-    _need(v_new, "v_new", (N, HEAD_DIM), bf16, device)
-    _need(s_new, "s_new", (N,), bf16, device)
+    pl = _need(ctx_len, "ctx_len", (S,), torch.int32, device)
+    pk = _need(k_new, "k_new", (N, HEAD_DIM), bf16, device)
+    pv = _need(v_new, "v_new", (N, HEAD_DIM), bf16, device)
+    ps = _need(s_new, "s_new", (N,), bf16, device)
+    pq = None
     if q_start is not None:
-        _need(q_start, "q_start", (S + 1,), torch.int32, device)
+        pq = _need(q_start, "q_start", (S + 1,), torch.int32, device)
     elif N != S:
         raise ValueError(f"{N} new tokens for {S} sequences need q_start")
-    return S, N
+    return pk, pv, ps, pq, pl, S, N
 
 
 def _attend_args(q, g, out, vha, rows, scale, device):
+    """(pointers of q and g, out, its pointer, scale, head-mix factors and rank)"""
     shape = (rows, HEADS, HEAD_DIM)
-    _need(q, "q", shape, torch.bfloat16, device)
-    _need(g, "g", shape, torch.bfloat16, device)
+    pq = _need(q, "q", shape, torch.bfloat16, device)
+    pg = _need(g, "g", shape, torch.bfloat16, device)
     if out is None:
         out = torch.empty_like(q)
+        po = out.data_ptr()
     else:
-        _need(out, "out", shape, torch.bfloat16, device)
+        po = _need(out, "out", shape, torch.bfloat16, device)
     down, up, r = (None, None, 0) if vha is None else _check_vha(vha, device)
-    return out, _SCALE if scale is None else scale, _ptr(down), _ptr(up), r
+    return pq, pg, out, po, _SCALE if scale is None else scale, _ptr(down), _ptr(up), r
 
 
 def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, s_new: torch.Tensor,
@@ -561,12 +556,11 @@ def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, s_new: torch.Tensor,
     [num_pages, page_size, 512]; page_table [S, max_pages] int32: entry j of
     sequence i is row j % page_size of page page_table[i, j // page_size]."""
     device = _device_of(wk, "wk")
-    S, N = _check_chunk(k_new, v_new, s_new, q_start, ctx_len, device)
+    chunk = _check_chunk(k_new, v_new, s_new, q_start, ctx_len, device)
+    S, N = chunk[5:]
     cache = _paged_cache(S, wk, wv, ws, ck_pages, cv_pages, page_table, device)
-    if N == 0:
-        return
-    _call(device, "hca_paged_append", k_new.data_ptr(), v_new.data_ptr(), s_new.data_ptr(),
-          _ptr(q_start), ctx_len.data_ptr(), S, N, ctypes.byref(cache))
+    if N > 0:
+        _call(device, "hca_paged_append", *chunk, cache)
 
 
 def paged_prefill_workspace(S: int, N: int, device) -> torch.Tensor:
@@ -591,16 +585,16 @@ def paged_prefill(q: torch.Tensor, g: torch.Tensor, k_new: torch.Tensor, v_new: 
     device = _device_of(wk, "wk")
     if q_start is None:
         raise ValueError("paged_prefill needs q_start (paged_decode_step takes one token each)")
-    S, N = _check_chunk(k_new, v_new, s_new, q_start, ctx_len, device)
+    chunk = _check_chunk(k_new, v_new, s_new, q_start, ctx_len, device)
+    S, N = chunk[5:]
     cache = _paged_cache(S, wk, wv, ws, ck_pages, cv_pages, page_table, device)
-    out, scale, down, up, r = _attend_args(q, g, out, vha, N, scale, device)
+    pq, pg, out, po, scale, down, up, r = _attend_args(q, g, out, vha, N, scale, device)
     if N == 0:
         return out
     if workspace is None:
         workspace = paged_prefill_workspace(S, N, device)
-    _call(device, "hca_paged_prefill", q.data_ptr(), g.data_ptr(), k_new.data_ptr(),
-          v_new.data_ptr(), s_new.data_ptr(), q_start.data_ptr(), ctx_len.data_ptr(), S, N, HEADS,
-          scale, down, up, r, ctypes.byref(cache), out.data_ptr(), *_workspace(workspace, device))
+    _call(device, "hca_paged_prefill", pq, pg, *chunk, HEADS, scale, down, up, r, cache, po,
+          *_workspace(workspace, device))
     return out
 
 
@@ -621,13 +615,13 @@ def paged_decode(q: torch.Tensor, ck_pages: torch.Tensor, cv_pages: torch.Tensor
     in comes from paged_decode_workspace."""
     device = _device_of(wk, "wk")
     S = ctx_len.shape[0]
-    _need(ctx_len, "ctx_len", (S,), torch.int32, device)
+    pl = _need(ctx_len, "ctx_len", (S,), torch.int32, device)
     cache = _paged_cache(S, wk, wv, None, ck_pages, cv_pages, page_table, device)
-    out, scale, down, up, r = _attend_args(q, g, out, vha, S, scale, device)
+    pq, pg, out, po, scale, down, up, r = _attend_args(q, g, out, vha, S, scale, device)
     if workspace is None:
         workspace = paged_decode_workspace(S, device)
-    _call(device, "hca_paged_decode", q.data_ptr(), g.data_ptr(), ctx_len.data_ptr(), S, HEADS,
-          scale, down, up, r, ctypes.byref(cache), out.data_ptr(), *_workspace(workspace, device))
+    _call(device, "hca_paged_decode", pq, pg, pl, S, HEADS, scale, down, up, r, cache, po,
+          *_workspace(workspace, device))
     return out
 
 
@@ -640,31 +634,31 @@ def paged_decode_step(q: torch.Tensor, g: torch.Tensor, k_new: torch.Tensor, v_n
     """One serving step: paged_append of one token per sequence (k_new, v_new
     [S, 512]; s_new [S]), then paged_decode of their queries q, g [S, 64, 512]."""
     device = _device_of(wk, "wk")
-    S, _ = _check_chunk(k_new, v_new, s_new, None, ctx_len, device)
+    pk, pv, ps, _, pl, S, _ = _check_chunk(k_new, v_new, s_new, None, ctx_len, device)
     cache = _paged_cache(S, wk, wv, ws, ck_pages, cv_pages, page_table, device)
-    out, scale, down, up, r = _attend_args(q, g, out, vha, S, scale, device)
+    pq, pg, out, po, scale, down, up, r = _attend_args(q, g, out, vha, S, scale, device)
     if workspace is None:
         workspace = paged_decode_workspace(S, device)
-    _call(device, "hca_paged_decode_step", q.data_ptr(), g.data_ptr(), k_new.data_ptr(),
-          v_new.data_ptr(), s_new.data_ptr(), ctx_len.data_ptr(), S, HEADS, scale, down, up, r,
-          ctypes.byref(cache), out.data_ptr(), *_workspace(workspace, device))
+    _call(device, "hca_paged_decode_step", pq, pg, pk, pv, ps, pl, S, HEADS, scale, down, up, r,
+          cache, po, *_workspace(workspace, device))
     return out
 
 
-def _page_table(page_table, n_pages, ref, page_size: int, device) -> _PageTable:
+def _page_table(page_table, n_pages, ref, page_size: int, device):
+    """(the packed hca_page_table_t, rows, pages)"""
     if page_size not in PAGE_SIZES:
         raise ValueError(f"pages must hold 16, 32, 64 or 128 entries, got {page_size}")
     rows, num = n_pages.shape[0], ref.shape[0]
-    _need(n_pages, "n_pages", (rows,), torch.int32, device)
-    _need(ref, "ref", (num,), torch.int32, device)
+    pn = _need(n_pages, "n_pages", (rows,), torch.int32, device)
+    pr = _need(ref, "ref", (num,), torch.int32, device)
     cols, stride = _check_table(page_table, rows, device)
-    return _PageTable(page_table.data_ptr(), stride, rows, cols, n_pages.data_ptr(),
-                      ref.data_ptr(), num, page_size)
+    return (_PAGE_TABLE(page_table.data_ptr(), stride, rows, cols, pn, pr, num, page_size), rows,
+            num)
 
 
-def _page_arrays(arrays, items: int, what: str, device):
+def _page_arrays(arrays, items: int, what: str, device) -> bytes:
     """Item arrays for the library: any dtype, contiguous, [items, ...]."""
-    out = (_PageArray * max(1, len(arrays)))()
+    out = b""
     for i, t in enumerate(arrays):
         if not isinstance(t, torch.Tensor) or t.device != device:
             raise ValueError(f"{what}[{i}] must be a tensor on {device}")
@@ -673,14 +667,14 @@ def _page_arrays(arrays, items: int, what: str, device):
         nbytes = t.nbytes // items
         if nbytes < 16 or nbytes % 16:
             raise ValueError(f"{what}[{i}]: items of {nbytes} bytes, a multiple of 16 is needed")
-        out[i].data, out[i].item_bytes = t.data_ptr(), nbytes
+        out += _PAGE_ARRAY(t.data_ptr(), nbytes)
     return out
 
 
 def _pages_workspace(workspace, rows, num_pages, n, device):
     if workspace is None:
-        workspace = torch.empty((_sized(device, "hca_pages_workspace_size", rows, num_pages, n),),
-                                dtype=torch.uint8, device=device)
+        size = lib().hca_pages_workspace_size(rows, num_pages, n)
+        workspace = torch.empty((size,), dtype=torch.uint8, device=device)
     return workspace
 
 
@@ -694,11 +688,10 @@ def resize_pages(page_table: torch.Tensor, n_pages: torch.Tensor, ref: torch.Ten
     shrink first; rows that grow take the lowest free pages, row by row, while
     there are any (n_pages[r] tells what row r has)."""
     device = _device_of(page_table, "page_table")
-    table = _page_table(page_table, n_pages, ref, page_size, device)
-    _need(entries, "entries", (table.rows,), torch.int32, device)
-    workspace = _pages_workspace(workspace, table.rows, table.num_pages, 0, device)
-    _call(device, "hca_pages_resize", ctypes.byref(table), entries.data_ptr(),
-          *_workspace(workspace, device))
+    table, rows, num = _page_table(page_table, n_pages, ref, page_size, device)
+    pe = _need(entries, "entries", (rows,), torch.int32, device)
+    workspace = _pages_workspace(workspace, rows, num, 0, device)
+    _call(device, "hca_pages_resize", table, pe, *_workspace(workspace, device))
 
 
 def fork_pages(page_table: torch.Tensor, n_pages: torch.Tensor, ref: torch.Tensor,
@@ -712,19 +705,19 @@ def fork_pages(page_table: torch.Tensor, n_pages: torch.Tensor, ref: torch.Tenso
     row children[i].  Returns ok [n] int32: 0 where no page was free (or the
     pair was refused, which device_error() reports)."""
     device = _device_of(page_table, "page_table")
-    table = _page_table(page_table, n_pages, ref, page_size, device)
+    table, rows, num = _page_table(page_table, n_pages, ref, page_size, device)
     n = parents.shape[0]
-    for t, name in ((parents, "parents"), (children, "children"), (entries, "entries")):
-        _need(t, name, (n,), torch.int32, device)
-    pool_arrays = _page_arrays(pools, table.num_pages, "pools", device)
-    ring_arrays = _page_arrays(rings, table.rows, "rings", device)
+    pp = _need(parents, "parents", (n,), torch.int32, device)
+    pc = _need(children, "children", (n,), torch.int32, device)
+    pe = _need(entries, "entries", (n,), torch.int32, device)
+    pool_arrays = _page_arrays(pools, num, "pools", device)
+    ring_arrays = _page_arrays(rings, rows, "rings", device)
     ok = torch.empty((n,), dtype=torch.int32, device=device)
     if n == 0:
         return ok
-    workspace = _pages_workspace(workspace, table.rows, table.num_pages, n, device)
-    _call(device, "hca_pages_fork", ctypes.byref(table), parents.data_ptr(), children.data_ptr(),
-          entries.data_ptr(), n, pool_arrays, len(pools), ring_arrays, len(rings), ok.data_ptr(),
-          *_workspace(workspace, device))
+    workspace = _pages_workspace(workspace, rows, num, n, device)
+    _call(device, "hca_pages_fork", table, pp, pc, pe, n, pool_arrays, len(pools), ring_arrays,
+          len(rings), ok.data_ptr(), *_workspace(workspace, device))
     return ok
 
 
@@ -734,11 +727,11 @@ def compact_pages(page_table: torch.Tensor, n_pages: torch.Tensor, ref: torch.Te
     ref and the contents of every pool ([num_pages, ...]) follow.  Returns the
     number of pages in use ([1] int32 on the device); all others are free."""
     device = _device_of(page_table, "page_table")
-    table = _page_table(page_table, n_pages, ref, PAGE_SIZES[0], device)
-    arrays = _page_arrays(pools, table.num_pages, "pools", device)
+    table, rows, num = _page_table(page_table, n_pages, ref, PAGE_SIZES[0], device)
+    arrays = _page_arrays(pools, num, "pools", device)
     live = torch.empty((1,), dtype=torch.int32, device=device)
-    workspace = _pages_workspace(workspace, table.rows, table.num_pages, 0, device)
-    _call(device, "hca_pages_compact", ctypes.byref(table), arrays, len(pools), live.data_ptr(),
+    workspace = _pages_workspace(workspace, rows, num, 0, device)
+    _call(device, "hca_pages_compact", table, arrays, len(pools), live.data_ptr(),
           *_workspace(workspace, device))
     return live
 
@@ -753,14 +746,14 @@ def copy_pages(arrays, src: torch.Tensor, dst: torch.Tensor,
         return
     device = _device_of(arrays[0], "arrays[0]")
     n, items = src.shape[0], arrays[0].shape[0]
-    _need(src, "src", (n,), torch.int32, device)
-    _need(dst, "dst", (n,), torch.int32, device)
+    ps = _need(src, "src", (n,), torch.int32, device)
+    pd = _need(dst, "dst", (n,), torch.int32, device)
     item_arrays = _page_arrays(arrays, items, "arrays", device)
     if n == 0:
         return
     workspace = _pages_workspace(workspace, 1, items, n, device)
-    _call(device, "hca_pages_copy", item_arrays, len(arrays), items, src.data_ptr(),
-          dst.data_ptr(), n, *_workspace(workspace, device))
+    _call(device, "hca_pages_copy", item_arrays, len(arrays), items, ps, pd, n,
+          *_workspace(workspace, device))
 
 
 def device_error(device: Optional[torch.device] = None) -> Tuple[int, int]:
