@@ -1,4 +1,5 @@
-"""Build libhca.so in-tree with nvcc for sm_100a.
+"""Build libhca.so in-tree with nvcc for sm_100a, and with g++ the module that makes
+the binding's paged calls (csrc/paged_calls.cpp, linked against it and torch).
 
 Usage:  python -m compressed_sliding_window_b200.build [--force]
 """
@@ -9,12 +10,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_PATH = os.path.join(PKG_DIR, "libhca.so")
 MAIN_SRC = os.path.join(CSRC, "hca_lib.cu")
+CALLS_PATH = os.path.join(PKG_DIR, "_paged_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+CALLS_SRC = os.path.join(CSRC, "paged_calls.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -42,7 +46,39 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(s) <= lib_m for s in _sources())
 
 
+def build_calls(force: bool = False, verbose: bool = False) -> str:
+    """The module behind the binding's paged calls (needs libhca.so)."""
+    srcs = [CALLS_SRC, os.path.join(ROOT, "include", "hca.h")]
+    if not force and os.path.exists(CALLS_PATH) and all(
+            os.path.getmtime(f) <= os.path.getmtime(CALLS_PATH) for f in srcs):
+        return CALLS_PATH
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = CALLS_PATH + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(base, "include"),
+           "-I" + os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-I" + os.path.join(cuda, "include"), CALLS_SRC, "-o", tmp, "-L" + PKG_DIR,
+           "-l:" + os.path.basename(LIB_PATH), "-L" + os.path.join(base, "lib"), "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, CALLS_PATH)
+    return CALLS_PATH
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    lib = _build_lib(force, verbose)
+    build_calls(force, verbose)
+    return lib
+
+
+def _build_lib(force: bool, verbose: bool) -> str:
     if not force and up_to_date():
         return LIB_PATH
     tmp = LIB_PATH + ".tmp"
