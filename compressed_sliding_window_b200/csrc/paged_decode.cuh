@@ -315,7 +315,9 @@ __device__ __forceinline__ void own_query(const long long* tiles, int S, int lon
     for (int i = lane; i < S; i += 32) x += parts_of(static_cast<int>(tiles[i + 1] - tiles[i]), inv);
     return __reduce_add_sync(0xffffffffu, x);
   };
-  int lo = max(1, static_cast<int>((tiles[S] + G - 1) / G)), hi = max(lo, longest);
+  // sum of ceil(t / T) < N / T + S: T = ceil(N / (G - S)) always fits
+  const int N = static_cast<int>(tiles[S]);
+  int lo = max(1, (N + G - 1) / G), hi = max(lo, min(longest, (N + G - S - 1) / (G - S)));
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (all_parts(mid) <= G) hi = mid; else lo = mid + 1;
@@ -554,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == kThreads - 32) {   // a warp with nothing to plan for, as a rule
     mbar_init(bar(B_QFULL), 1);
     mbar_init(bar(B_QEMPTY), 1);
     for (int s = 0; s < kStages; ++s) {
@@ -1067,29 +1069,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok) ok = mbar_wait_warp(bar(B_OFULL), nseg & 1, abort_flag, kWaitLimitNs, 62);
         tc_fence_after();
-        float* wo = p.ws_o + slot * kHeads * kDim + lane;
-        float* keep = reinterpret_cast<float*>(smem + merge_data(parts)) + 512 * nk * part + lane;
-        auto chunk_at = [&](int k) -> float* {
-          return kept && k >= k0 && k < k0 + nk ? keep + 512 * (k - k0) : wo + 512 * k;
-        };
+        float* wo = p.ws_o + slot * kHeads * kDim;
+        float* keep = reinterpret_cast<float*>(smem + merge_data(parts)) + 512 * nk * part;
+        // A chunk goes through this warp's 2 KB of the P^T buffer and leaves 16 bytes a
+        // lane: 4-byte stores to global memory took 2.8 us a partial (25 bytes a cycle).
+        float* stage = reinterpret_cast<float*>(smem + kSmemPT) + 512 * sw;
         float inv[32];
         load_row<32>(mrow + 32, inv);      // before the stores, which it could not pass
 #pragma unroll 1
-        for (int i = 0; i < 2; ++i) {      // value columns 256 i + key and 256 i + 128 + key
-          uint32_t o[64];
-          tmem_ld32(tl + kTmemO + 128 * i, o);
-          tmem_ld32(tl + kTmemO + 128 * i + 64, o + 32);
+        for (int c = 0; c < 4; ++c) {      // value columns 128 c + key
+          uint32_t o[32];
+          tmem_ld32(tl + kTmemO + 64 * c, o);
           tmem_wait_ld_dep32(o);
-          reg_dep32(o + 32);
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+          for (int hb = 0; hb < 2; ++hb) {
+            const int k = 16 * (2 * half + hb) + 4 * c + wq;
+            const bool here = kept && k >= k0 && k < k0 + nk;
+            float* dst = here ? keep + 512 * (k - k0) : stage;
 #pragma unroll
-            for (int hb = 0; hb < 2; ++hb) {
-              float* dst = chunk_at(16 * (2 * half + hb) + 4 * (2 * i + c) + wq);
+            for (int h = 0; h < 16; ++h)
+              dst[32 * h + lane] = __uint_as_float(o[16 * hb + h]) * inv[16 * hb + h];
+            if (!here) {
+              __syncwarp();
+              float4* g4 = reinterpret_cast<float4*>(wo + 512 * k) + lane;
+              float4 v[4];
 #pragma unroll
-              for (int h = 0; h < 16; ++h)
-                dst[32 * h] = __uint_as_float(o[32 * c + 16 * hb + h]) * inv[16 * hb + h];
+              for (int q = 0; q < 4; ++q) v[q] = reinterpret_cast<const float4*>(stage)[32 * q + lane];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) g4[32 * q] = v[q];
+              __syncwarp();
             }
+          }
         }
         // the partial is written: one arrival for the CTAs that share the query
         named_bar_sync(3, 32 * kSoftWarps);
