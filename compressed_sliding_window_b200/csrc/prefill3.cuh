@@ -717,6 +717,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       return n_uses;
     };
     const int orow0 = 2 * half;   // first position of this CTA's rows
+    // Ring stage st is always loaded by producer warp st & 1, so that this warp waits
+    // for every phase of its "empty" barrier, one after the other.  A parity wait
+    // only tells a phase from its neighbours: a warp that comes by at every other
+    // use of a stage (as with uses dealt out in turn over 5 stages) and does so
+    // while the use two back has not been released -- gate stages are released
+    // behind stages used after them -- would pass at once and load over it.
     if (warp <= 1) {
       // --------------------------------------------------------- producers
       if constexpr (kPaged) {
@@ -753,10 +759,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
               bytes[h] = 2u * 2u * (((nh + (1 << rsh[h]) - 1) >> rsh[h]) << rsh[h]) * 128u;
             }
             for (int s = 0; s < nst && ok; ++s, ++u) {
-              if ((u & 1) != static_cast<uint32_t>(me)) continue;
+              const uint32_t st = u % NV;
+              if ((st & 1) != static_cast<uint32_t>(me)) continue;   // see above: one warp a stage
               int dh, h;
               pv_stage(s, two, j == 0 || j == x.ntiles - 1, dh, h);
-              const uint32_t st = u % NV;
               const uint32_t fb = lbar(VFULL + st);
               const bool wtail = !comp && h == 1;          // raw keys t0 + 1 .. t0 + 16
               if (lane == 0) {
@@ -791,8 +797,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
           for (int g = 0; g < 4 && ok; ++g, ++u) {   // gate stages of this CTA's rows
-            if ((u & 1) != static_cast<uint32_t>(me)) continue;
             const uint32_t st = u % NV;
+            if ((st & 1) != static_cast<uint32_t>(me)) continue;
             if (lane == 0) {
               ok = mbar_wait(bar(VEMPTY + st), ((u / NV) & 1) ^ 1, abort_flag, kWaitLimitNs, 341);
               if (ok) {
@@ -821,10 +827,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             const bool two = sub_n(n, 1) > 0;
             const int nst = two ? 4 : 2;
             for (int s = 0; s < nst && ok; ++s, ++u) {
-              if ((u & 1) != static_cast<uint32_t>(me)) continue;
+              const uint32_t st = u % NV;
+              if ((st & 1) != static_cast<uint32_t>(me)) continue;   // see above: one warp a stage
               int dh, h;
               pv_stage(s, two, j == 0 || j == x.ntiles - 1, dh, h);
-              const uint32_t st = u % NV;
               ok = mbar_wait(bar(VEMPTY + st), ((u / NV) & 1) ^ 1, abort_flag, kWaitLimitNs,
                              340);
               if (!ok) break;
@@ -848,8 +854,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
           }
 #pragma unroll 1
           for (int e = 0; e < 4 && ok; ++e, ++u) {   // gate stages of this CTA's rows
-            if ((u & 1) != static_cast<uint32_t>(me)) continue;
             const uint32_t st = u % NV;
+            if ((st & 1) != static_cast<uint32_t>(me)) continue;
             ok = mbar_wait(bar(VEMPTY + st), ((u / NV) & 1) ^ 1, abort_flag, kWaitLimitNs,
                            341);
             if (!ok) break;
@@ -1150,7 +1156,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         for (int e2 = 0; e2 < (helper ? 2 : 1); ++e2) {
           const int e = helper ? 2 + e2 : kv;   // g / out stage: value columns [128e, 128e + 128)
           const uint32_t st = (gbase + e) % NV;
-          if (!mbar_wait_warp(bar(GFULL + st), (gwait >> e) & 1u, abort_flag, kWaitLimitNs, 364)) {
+          // the stage's last gate use may have been another warp's: its phase first
+          if (!mbar_wait_warp(bar(GFULL + st), ((gwait >> e) & 1u) ^ 1u, abort_flag, kWaitLimitNs,
+                              364) ||
+              !mbar_wait_warp(bar(GFULL + st), (gwait >> e) & 1u, abort_flag, kWaitLimitNs, 364)) {
             ok = false;
             break;
           }
