@@ -111,7 +111,7 @@ constexpr int BAR = 229376;
 enum {
   QFULL = 0, QEMPTY = 2, KFULL = 4, KEMPTY = KFULL + kKStages, SFULL = KEMPTY + kKStages,
   SFREE = SFULL + 2, PFREE = SFREE + 2, STATSFREE = PFREE + 4,
-  VFULL = STATSFREE + 1, GFULL = VFULL + kVStages, VEMPTY = GFULL + kVStages,
+  VFULL = STATSFREE + 1, GFULL = VFULL + kVStages, VEMPTY = GFULL + 8,
   PREADY = VEMPTY + kVStages, PFULL = PREADY + 4, PBUFFREE = PFULL + 2, CORR = PBUFFREE + 2,
   PVDONE = CORR + 2, OFULL = PVDONE + 2, OFREE = OFULL + 2, STATSFULL = OFREE + 2,
   STAGED = STATSFULL + 1, XSTAGED = STAGED + 4, VHADONE = XSTAGED + 4, DRAIN = VHADONE + 4,
@@ -729,9 +729,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         // as on the S-CTAs: lane 8 s + r loads box r of slab s
         const int me = warp;
         const int bx = lane & 7, slab = lane >> 3;
-        uint32_t u = 0;
+        uint32_t u = 0, nitem = 0;
         bool ok = true;
-        for (int it = cluster; it < items && ok; it += nclusters) {
+        for (int it = cluster; it < items && ok; it += nclusters, ++nitem) {
           const Item x = decode_item<kPaged>(p, it);
           const int tail = p.tail16[x.seq];
           if (me == 0 && lane < 4)
@@ -802,8 +802,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             if (lane == 0) {
               ok = mbar_wait(bar(VEMPTY + st), ((u / NV) & 1) ^ 1, abort_flag, kWaitLimitNs, 341);
               if (ok) {
-                mbar_expect_tx(bar(GFULL + st), kVStage);
-                tma_load_4d(sb + O_VRING + st * kVStage, &maps.g4, bar(GFULL + st), 0,
+                const uint32_t gb = bar(GFULL + 4 * (nitem & 1) + g);
+                mbar_expect_tx(gb, kVStage);
+                tma_load_4d(sb + O_VRING + st * kVStage, &maps.g4, gb, 0,
                             (x.tok + orow0) * kHeads, 2 * g, 0);
               }
             }
@@ -812,9 +813,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         }
       } else if (lane == 0) {
         const int me = warp;
-        uint32_t u = 0;
+        uint32_t u = 0, nitem = 0;
         bool ok = true;
-        for (int it = cluster; it < items && ok; it += nclusters) {
+        for (int it = cluster; it < items && ok; it += nclusters, ++nitem) {
           const Item x = decode_item<kPaged>(p, it);
           if (me == 0) {  // warm L2 with this item's gate rows; they are staged after its V
 #pragma unroll 1
@@ -859,8 +860,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             ok = mbar_wait(bar(VEMPTY + st), ((u / NV) & 1) ^ 1, abort_flag, kWaitLimitNs,
                            341);
             if (!ok) break;
-            mbar_expect_tx(bar(GFULL + st), kVStage);
-            tma_load_4d(sb + O_VRING + st * kVStage, &maps.g4, bar(GFULL + st), 0,
+            const uint32_t gb = bar(GFULL + 4 * (nitem & 1) + e);
+            mbar_expect_tx(gb, kVStage);
+            tma_load_4d(sb + O_VRING + st * kVStage, &maps.g4, gb, 0,
                         (x.t0 + orow0) * kHeads, 2 * e, x.b);
           }
         }
@@ -1086,7 +1088,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       const volatile float* alpha_s = reinterpret_cast<const volatile float*>(smem + O_ALPHA);
       const volatile float* invl_s = reinterpret_cast<const volatile float*>(smem + O_INVL);
       const uint32_t partnerStatsFree = mapa_shared(bar(STATSFREE), rank - 2);
-      uint32_t sj = 0, nitem = 0, ubase = 0, ncorr = 0, gpar = 0;
+      uint32_t sj = 0, nitem = 0, ubase = 0, ncorr = 0;
       bool ok = true;
       for (int it = cluster; it < items && ok; it += nclusters, ++nitem) {
         const Item x = decode_item<kPaged>(p, it);
@@ -1143,23 +1145,15 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t gbase = ubase + v_uses(x);
         ubase = gbase + 4;
-        // parity of each gate stage's use count so far (every epilogue warp
-        // walks all four stages' uses, reading only its own)
-        uint32_t gwait = 0;   // bit e: the wait parity of gate stage e
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t st = (gbase + e) % NV;
-          gwait |= ((gpar >> st) & 1u) << e;
-          gpar ^= 1u << st;
-        }
 #pragma unroll 1
         for (int e2 = 0; e2 < (helper ? 2 : 1); ++e2) {
           const int e = helper ? 2 + e2 : kv;   // g / out stage: value columns [128e, 128e + 128)
           const uint32_t st = (gbase + e) % NV;
-          // the stage's last gate use may have been another warp's: its phase first
-          if (!mbar_wait_warp(bar(GFULL + st), ((gwait >> e) & 1u) ^ 1u, abort_flag, kWaitLimitNs,
-                              364) ||
-              !mbar_wait_warp(bar(GFULL + st), (gwait >> e) & 1u, abort_flag, kWaitLimitNs, 364)) {
+          // GFULL belongs to (item parity, e), not to the ring stage: its waiters are the
+          // same warps every time and see each of its phases, and the next load on it is
+          // two items on, behind their OFREE arrival of the item between
+          if (!mbar_wait_warp(bar(GFULL + 4 * (nitem & 1) + e), (nitem >> 1) & 1, abort_flag,
+                              kWaitLimitNs, 364)) {
             ok = false;
             break;
           }
