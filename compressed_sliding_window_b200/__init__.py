@@ -473,6 +473,15 @@ def _device_of(t: torch.Tensor, name: str) -> torch.device:
     return t.device
 
 
+def _rows(t: torch.Tensor, name: str, dims: int) -> int:
+    """Rows of a tensor that has `dims` dimensions."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimension(s), got shape {tuple(t.shape)}")
+    return t.shape[0]
+
+
 def _call(device: torch.device, name: str, *args):
     """A library call on the current stream of `device`, made the current device for it."""
     if torch.cuda.current_device() == device.index:
@@ -498,7 +507,7 @@ def _cuda(device) -> torch.device:
 
 
 def _workspace(workspace: torch.Tensor, device):
-    n = workspace.numel()
+    n = _rows(workspace, "workspace", 1)
     return _need(workspace, "workspace", (n,), torch.uint8, device), n
 
 
@@ -537,8 +546,8 @@ def _paged_cache(S, wk, wv, ws, ck_pages, cv_pages, page_table, device) -> bytes
 
 def _check_chunk(k_new, v_new, s_new, q_start, ctx_len, device):
     """(pointers of k_new, v_new, s_new, q_start, ctx_len, then S, N)"""
-    S = ctx_len.shape[0]
-    N = k_new.shape[0]
+    S = _rows(ctx_len, "ctx_len", 1)
+    N = _rows(k_new, "k_new", 2)
     bf16 = torch.bfloat16
     pl = _need(ctx_len, "ctx_len", (S,), torch.int32, device)
     pk = _need(k_new, "k_new", (N, HEAD_DIM), bf16, device)
@@ -651,7 +660,7 @@ def paged_decode(q: torch.Tensor, ck_pages: torch.Tensor, cv_pages: torch.Tensor
         if r is not False:
             return r if type(r) is not int else _raise("hca_paged_decode", r)
     device = _device_of(wk, "wk")
-    S = ctx_len.shape[0]
+    S = _rows(ctx_len, "ctx_len", 1)
     pl = _need(ctx_len, "ctx_len", (S,), torch.int32, device)
     cache = _paged_cache(S, wk, wv, None, ck_pages, cv_pages, page_table, device)
     pq, pg, out, po, scale, down, up, r = _attend_args(q, g, out, vha, S, scale, device)
@@ -690,7 +699,7 @@ def _page_table(page_table, n_pages, ref, page_size: int, device):
     """(the packed hca_page_table_t, rows, pages)"""
     if page_size not in PAGE_SIZES:
         raise ValueError(f"pages must hold 16, 32, 64 or 128 entries, got {page_size}")
-    rows, num = n_pages.shape[0], ref.shape[0]
+    rows, num = _rows(n_pages, "n_pages", 1), _rows(ref, "ref", 1)
     pn = _need(n_pages, "n_pages", (rows,), torch.int32, device)
     pr = _need(ref, "ref", (num,), torch.int32, device)
     cols, stride = _check_table(page_table, rows, device)
@@ -755,7 +764,7 @@ def fork_pages(page_table: torch.Tensor, n_pages: torch.Tensor, ref: torch.Tenso
         return r if type(r) is not int else _raise("hca_pages_fork", r)
     device = _device_of(page_table, "page_table")
     table, rows, num = _page_table(page_table, n_pages, ref, page_size, device)
-    n = parents.shape[0]
+    n = _rows(parents, "parents", 1)
     pp = _need(parents, "parents", (n,), torch.int32, device)
     pc = _need(children, "children", (n,), torch.int32, device)
     pe = _need(entries, "entries", (n,), torch.int32, device)
@@ -797,7 +806,7 @@ def copy_pages(arrays, src: torch.Tensor, dst: torch.Tensor,
     if len(arrays) == 0:
         return
     device = _device_of(arrays[0], "arrays[0]")
-    n, items = src.shape[0], arrays[0].shape[0]
+    n, items = _rows(src, "src", 1), arrays[0].shape[0] if arrays[0].dim() else 0
     ps = _need(src, "src", (n,), torch.int32, device)
     pd = _need(dst, "dst", (n,), torch.int32, device)
     item_arrays = _page_arrays(arrays, items, "arrays", device)

@@ -102,7 +102,10 @@ struct Args {
     p.rows = static_cast<int>(rows);
     p.max_pages = static_cast<int>(cols);
     p.num_pages = static_cast<int>(num);
-    p.page_size = good ? static_cast<int>(PyLong_AsLong(page_size)) : 0;
+    int overflow = 0;
+    const long size = good ? PyLong_AsLongAndOverflow(page_size, &overflow) : 0;
+    good = good && overflow == 0 && size >= 0 && size <= INT_MAX;
+    p.page_size = static_cast<int>(size);
   }
   // a tuple or list of [items, ...] tensors appended to out[n ..]
   int arrays(PyObject* seq, int64_t items, hca_page_array_t* out, int n, int most) {

@@ -402,9 +402,9 @@ size_t hca_paged_prefill_workspace_size(int S, int N);
  *          hca_paged_prefill_workspace_size(S, N) bytes, 256-byte aligned,
  *          zero-filled before its first use (every call leaves it valid for
  *          the next, whatever its S and N); calls that overlap need one each.
- *          A token's values must be finite: one that is not may also reach the
- *          outputs of up to 16 positions before it in its sequence, and
- *          nothing else's.
+ *          Tokens must be finite: one that is not may also reach outputs of
+ *          its sequence, in this call or a later one, that give it no weight
+ *          (zero times infinity is NaN); other sequences are not touched.
  * Errors:  those of hca_paged_append (q_start is required), of hca_decode_vha,
  *          and HCA_ERR_UNSUPPORTED for S > 4096 or (N + 144 S) * 64 >= 2^31.
  */
