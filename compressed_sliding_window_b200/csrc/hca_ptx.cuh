@@ -458,6 +458,14 @@ __device__ __forceinline__ void cluster_sync_all() {
                    : "memory");
 }
 
+// the two halves of cluster_sync_all
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // tcgen05.commit that arrives on the mbarrier at the same shared-memory offset
 // in every CTA of `cta_mask` (cluster).
 __device__ __forceinline__ void umma_commit_mc(uint32_t bar, uint16_t cta_mask) {

@@ -10,13 +10,14 @@
 //   w = softmax(s), ck = sum w k, cv = sum w v ('BaiduがERNIE 5.5 Flash Baseを
 //   公開' §2.1), its tokens taken from the ring (positions before L0) and from
 //   the chunk.  Same thread layout and order of sums as the whole-sequence
-//   compressor, so the entries are bit-identical to it.  With kRaw it also
-//   lays the 127 tokens before the chunk, the chunk and 17 zero rows one after
+//   compressor, so the entries are bit-identical to it.  Without kRaw it is the
+//   whole append: the ring takes the newest tokens as well.  With kRaw it lays
+//   the 127 tokens before the chunk, the chunk and 17 zero rows one after
 //   another in the workspace, where the attention of the chunk reads the raw
-//   windows of all its tokens as contiguous rows.
-// finish_kernel, launched behind it: the ring takes the newest tokens (it may
-//   only change once every entry has been formed), and the queries' lengths,
-//   table rows and window rows are written for the attention.
+//   windows of all its tokens as contiguous rows;
+// finish_kernel, launched behind that, updates the ring (which may only change
+//   once the rows before the chunk have been read) and writes the item list and
+//   the copies of last pages for the attention.
 //
 // Both move bytes only: 2 KB a token in (and out again with kRaw).
 #pragma once
@@ -32,7 +33,9 @@ constexpr int kBlk = 128;
 constexpr int kBack = 127;      // tokens before the chunk that its first window needs
 constexpr int kPad = 144;       // workspace rows of a sequence beyond its n tokens
 constexpr int kThreads = 128;
-constexpr int kUnitsExtra = 4;  // blocks that n + kPad rows can touch beyond n / 128
+// blocks that n + kPad rows (kRaw), or n, can touch beyond n / 128
+template <bool kRaw>
+constexpr int kUnitsExtra = kRaw ? 4 : 2;
 
 struct Cache {
   uint16_t* wk;        // [S, 128, 512]
@@ -94,23 +97,37 @@ __device__ __forceinline__ long long entry_row(const Cache& c, int i, int j, uns
 }
 
 // Sequence of work unit u when sequence i owns the units from
-// floor(q_start[i] / 128) + 4 i on (at least as many as it can need): found by
-// counting, every thread a share of the offsets, without a prefix sum.
-__device__ __forceinline__ int unit_seq(const Chunk& c, int u, int* red) {
-  int cnt = 0;
-  for (int i = threadIdx.x; i < c.S; i += kThreads) {
+// floor(q_start[i] / 128) + extra i on (at least as many as it can need): the last that
+// does not start behind u, found by counting in two rounds, every 1/128th of the offsets
+// and then the 1/128th that it names (one round up to 128 sequences), without a prefix
+// sum.  Counting all offsets took 90 us for 2000 sequences of a token or two.
+__device__ __forceinline__ int unit_seq(const Chunk& c, int u, int extra, int* red) {
+  auto count = [&](bool in) -> int {
+    const unsigned some = __ballot_sync(0xffffffffu, in);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = __popc(some);
+    __syncthreads();
+    return red[0] + red[1] + red[2] + red[3];
+  };
+  auto starts = [&](int i) -> bool {   // at or before u
     const int qs = c.q_start != nullptr ? min(max(c.q_start[i], 0), c.N) : i;
-    cnt += (qs / kBlk + kUnitsExtra * i <= u) ? 1 : 0;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = cnt;
-  __syncthreads();
-  cnt = red[0] + red[1] + red[2] + red[3];
-  return max(cnt - 1, 0);
+    return qs / kBlk + extra * i <= u;
+  };
+  const int step = (c.S + kThreads - 1) / kThreads, tid = threadIdx.x;
+  int at = max(count(tid * step < c.S && starts(tid * step)) - 1, 0) * step;
+  const int end = min(at + step, c.S);
+  for (int base = at + 1; base < end; base += kThreads)
+    at += count(base + tid < end && starts(base + tid));
+  return at;
 }
 
-// grid.x = floor(N / 128) + 4 S units, grid.y = 8 (K/V x 4 channel quarters)
+// Newest position of ring slot `slot` with L1 tokens.
+__device__ __forceinline__ int newest(int L1, int slot) {
+  return L1 - 1 - ((L1 - 1 - slot) & (kBlk - 1));
+}
+
+// grid.x = floor(N / 128) + kUnitsExtra S units, grid.y = 8 (K/V x 4 channel quarters);
+// without kRaw the 8 CTAs of a unit are a cluster
 template <bool kRaw>
 __global__ void __launch_bounds__(kThreads)
     entries_kernel(const Chunk c, const Cache cache, uint16_t* __restrict__ raw_k,
@@ -123,16 +140,22 @@ __global__ void __launch_bounds__(kThreads)
   const int tid = threadIdx.x, warp = tid >> 5;
   const int u = blockIdx.x;
   const int which = blockIdx.y >> 2, quarter = blockIdx.y & 3;
-  const int i = unit_seq(c, u, cnt);
+  const int i = unit_seq(c, u, kUnitsExtra<kRaw>, cnt);
   const Span sp = span_of(c, i, false);
-  const int ubase = sp.qs / kBlk + kUnitsExtra * i;
+  if (!kRaw && u == 0 && blockIdx.y == 0)
+    for (int j = tid; j < c.S; j += kThreads) span_of(c, j, true);
+  const int ubase = sp.qs / kBlk + kUnitsExtra<kRaw> * i;
   if (u < ubase || sp.n == 0) return;
-  // block b, positions p0 .. p0 + 127; the first block is that of position L0 - 127
-  const int b = ((sp.L0 - kBack + kBlk) >> 7) - 1 + (u - ubase);
+  // block b, positions p0 .. p0 + 127; the first block is that of position L0 - 127 (kRaw) or L0
+  const int b = (kRaw ? ((sp.L0 - kBack + kBlk) >> 7) - 1 : sp.L0 >> 7) + (u - ubase);
   const int p0 = b * kBlk;
   if (p0 > sp.L1 + 16) return;
   const bool completes = b >= 0 && p0 + kBlk <= sp.L1 && p0 + kBlk > sp.L0;
-  if (!kRaw && !completes) return;
+  // Only the block of the first new token takes tokens from the ring: its CTAs bring the
+  // ring up to date, each the channels that it reads itself, so that only the scores, which
+  // all of them read and one writes, make them wait for one another.
+  const bool renews = !kRaw && u == ubase;
+  if (!kRaw && !completes && !renews) return;
 
   if (completes) {   // within-block softmax of the scores (fp32)
     const int p = p0 + tid;
@@ -150,10 +173,11 @@ __global__ void __launch_bounds__(kThreads)
     z = red[1][0] + red[1][1] + red[1][2] + red[1][3];
     w[tid] = e / z;
     __syncthreads();
+    if (renews) cluster_arrive();   // the scores have been read
   }
 
   // thread (r, c): tokens r, r + 8, .. and channels 8 c .. 8 c + 7 of the quarter
-  const uint16_t* ring = (which ? cache.wv : cache.wk) + static_cast<size_t>(i) * kBlk * kD;
+  uint16_t* ring = (which ? cache.wv : cache.wk) + static_cast<size_t>(i) * kBlk * kD;
   const uint16_t* fresh = (which ? c.v : c.k) + static_cast<size_t>(sp.qs) * kD;
   uint16_t* raw = which ? raw_v : raw_k;
   const int col = quarter * 128 + (tid & 15) * 8;
@@ -163,6 +187,7 @@ __global__ void __launch_bounds__(kThreads)
   for (int q = 0; q < 16; ++q) {
     const int p = p0 + q * 8 + r;
     x[q] = make_uint4(0u, 0u, 0u, 0u);
+    if (!kRaw && !completes) continue;
     if (p >= sp.L0) {
       if (p < sp.L1)
         x[q] = __ldg(reinterpret_cast<const uint4*>(fresh + static_cast<size_t>(p - sp.L0) * kD + col));
@@ -179,30 +204,48 @@ __global__ void __launch_bounds__(kThreads)
         *reinterpret_cast<uint4*>(raw + (row0 + p) * kD + col) = x[q];
     }
   }
-  if (!completes) return;
-  float acc[8];
+  if (renews) {   // a thread writes the ring where it read it
 #pragma unroll
-  for (int a = 0; a < 8; ++a) acc[a] = 0.f;
-#pragma unroll
-  for (int q = 0; q < 16; ++q) {
-    const float wi = w[q * 8 + r];
-    const uint32_t uu[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      acc[2 * a] = fmaf(wi, bf16lo_to_f32(uu[a]), acc[2 * a]);
-      acc[2 * a + 1] = fmaf(wi, bf16hi_to_f32(uu[a]), acc[2 * a + 1]);
+    for (int q = 0; q < 16; ++q) {
+      const int p = newest(sp.L1, q * 8 + r);
+      if (p >= sp.L0)
+        *reinterpret_cast<uint4*>(ring + static_cast<size_t>(q * 8 + r) * kD + col) =
+            __ldg(reinterpret_cast<const uint4*>(fresh + static_cast<size_t>(p - sp.L0) * kD + col));
     }
   }
+  if (completes) {
+    float acc[8];
 #pragma unroll
-  for (int a = 0; a < 8; ++a) part[r][(tid & 15) * 8 + a] = acc[a];
-  __syncthreads();
-  float tot = 0.f;
+    for (int a = 0; a < 8; ++a) acc[a] = 0.f;
 #pragma unroll
-  for (int rr = 0; rr < 8; ++rr) tot += part[rr][tid];
-  const long long row = entry_row(cache, i, b, 211);
-  if (row < 0) return;
-  __nv_bfloat16 hb = __float2bfloat16_rn(tot);
-  (which ? cache.cv : cache.ck)[row * kD + quarter * 128 + tid] = *reinterpret_cast<uint16_t*>(&hb);
+    for (int q = 0; q < 16; ++q) {
+      const float wi = w[q * 8 + r];
+      const uint32_t uu[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        acc[2 * a] = fmaf(wi, bf16lo_to_f32(uu[a]), acc[2 * a]);
+        acc[2 * a + 1] = fmaf(wi, bf16hi_to_f32(uu[a]), acc[2 * a + 1]);
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < 8; ++a) part[r][(tid & 15) * 8 + a] = acc[a];
+    __syncthreads();
+    float tot = 0.f;
+#pragma unroll
+    for (int rr = 0; rr < 8; ++rr) tot += part[rr][tid];
+    const long long row = entry_row(cache, i, b, 211);
+    if (row >= 0) {
+      __nv_bfloat16 hb = __float2bfloat16_rn(tot);
+      (which ? cache.cv : cache.ck)[row * kD + quarter * 128 + tid] =
+          *reinterpret_cast<uint16_t*>(&hb);
+    }
+    if (renews) cluster_wait();
+  }
+  if (renews && blockIdx.y == 0) {
+    const int p = newest(sp.L1, tid);
+    if (p >= sp.L0)
+      cache.ws[static_cast<size_t>(i) * kBlk + tid] = c.s[static_cast<size_t>(sp.qs) + (p - sp.L0)];
+  }
 }
 
 constexpr int kFinishY = 8;     // CTAs of a sequence, 16 ring slots each
@@ -289,7 +332,7 @@ __global__ void __launch_bounds__(kFinishThreads)
   for (int q = 0; q < kSlots * 2 * 64 / kFinishThreads; ++q) {
     const int idx = q * kFinishThreads + tid;
     const int slot = blockIdx.y * kSlots + (idx >> 7), which = (idx >> 6) & 1, col = (idx & 63) * 8;
-    const int p = sp.L1 - 1 - ((sp.L1 - 1 - slot) & (kBlk - 1));   // newest position of the slot
+    const int p = newest(sp.L1, slot);
     if (sp.n > 0 && p >= sp.L0) {
       const size_t tok = static_cast<size_t>(sp.qs) + (p - sp.L0);
       const size_t dst = (static_cast<size_t>(i) * kBlk + slot) * kD + col;

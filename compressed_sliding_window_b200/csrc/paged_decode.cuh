@@ -1121,7 +1121,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   }  // A0 < A1
-  if (threadIdx.x == 0) abort_drain(abort_flag);
+  if (threadIdx.x == 0) {
+    abort_drain(abort_flag);
+    // whoever follows this kernel may count on the one before it being done, too
+    if (p.only_window) asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
   __syncthreads();
   if (warp == kProducers) {
     tc_fence_after();

@@ -76,8 +76,9 @@ cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, cudaStre
 }
 
 // grid.x of entries_kernel: the units of all sequences
+template <bool kRaw>
 long long entry_units(int S, int N) {
-  return N / hca::paged::kBlk + static_cast<long long>(hca::paged::kUnitsExtra) * S;
+  return N / hca::paged::kBlk + static_cast<long long>(hca::paged::kUnitsExtra<kRaw>) * S;
 }
 
 // The zero-filled head of a workspace, the same for every call: grid barrier,
@@ -295,12 +296,21 @@ hca_status_t hca_paged_append(const hca_bf16* k_new, const hca_bf16* v_new, cons
     G::step_kernel<<<dim3(S, 8), G::kThreads, 0, stream>>>(ch, c);
     return launch_status();
   }
-  const long long units = entry_units(S, N);
+  const long long units = entry_units<false>(S, N);
   if (units > 0x7fffffffLL) return HCA_ERR_UNSUPPORTED;
-  G::entries_kernel<false>
-      <<<dim3(static_cast<unsigned>(units), 8), G::kThreads, 0, stream>>>(ch, c, nullptr, nullptr);
-  if (launch_behind(G::finish_kernel, dim3(S, G::kFinishY), G::kFinishThreads, stream, ch, c,
-                    G::Queries{}) != cudaSuccess)
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(units), 8);
+  cfg.blockDim = dim3(G::kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 1;
+  attr.val.clusterDim.y = 8;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  uint16_t* none = nullptr;
+  if (cudaLaunchKernelEx(&cfg, G::entries_kernel<false>, ch, c, none, none) != cudaSuccess)
     return HCA_ERR_CUDA;
   return launch_status();
 }
@@ -335,7 +345,7 @@ hca_status_t hca_paged_prefill(const hca_bf16* q, const hca_bf16* g, const hca_b
   if (S > kMaxChunkSeqs || static_cast<long long>(N) + static_cast<long long>(G::kPad) * S >
                                0x7fffffffLL / HCA_NUM_HEADS)
     return HCA_ERR_UNSUPPORTED;
-  const long long units = entry_units(S, N);
+  const long long units = entry_units<true>(S, N);
   const int most = prefill_max_clusters<true>();
   if (most <= 0) return HCA_ERR_CUDA;
   const PagedPrefillLayout L = paged_prefill_layout(S, N, most);
