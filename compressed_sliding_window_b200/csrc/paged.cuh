@@ -343,34 +343,23 @@ __global__ void __launch_bounds__(kFinishThreads)
   }
 }
 
-// One token a sequence (ring write and, where a block completes, its entry) in
-// one launch: grid (S, 8), CTA (i, y) = (K or V, channel quarter) of sequence i,
-// 128 threads.  Latency-bound.  Each CTA reads and writes its own channels of
-// the ring; the newest row and score are taken from the inputs, so no CTA
-// waits for another's ring write.
-__global__ void __launch_bounds__(kThreads) step_kernel(const Chunk c, const Cache cache) {
-  __shared__ float w[kBlk];
-  __shared__ float red[2][4];
-  __shared__ float part[8][kBlk + 4];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int i = blockIdx.x, tid = threadIdx.x, warp = tid >> 5;
-  const int which = blockIdx.y >> 2, quarter = blockIdx.y & 3;
-  const int L = c.ctx_len[i];
-  if (L < 1) {
-    if (tid == 0 && blockIdx.y == 0) record_error(DEVERR_BAD_INPUT, 212);
-    return;
-  }
-  const int slot = (L - 1) & (kBlk - 1);
-  uint16_t* ring = (which ? cache.wv : cache.wk) + static_cast<size_t>(i) * kBlk * kD;
+// One token a sequence, which completes a block: the ring is that block, its newest row
+// in slot 127.  K or V and channel quarter y of sequence i by 128 threads that `sync`
+// joins; the newest row and score come from the inputs, so that nobody waits for the
+// ring's update.
+struct RingScratch {
+  float w[kBlk];
+  float red[2][4];
+  float part[8][kBlk + 4];
+};
+template <typename Sync>
+__device__ __forceinline__ void entry_of_ring(const Chunk& c, const Cache& cache, int i, int L,
+                                              int y, int tid, RingScratch& sm, Sync sync) {
+  const int warp = tid >> 5, which = y >> 2, quarter = y & 3;
+  const uint16_t* ring = (which ? cache.wv : cache.wk) + static_cast<size_t>(i) * kBlk * kD;
   const uint16_t* fresh = (which ? c.v : c.k) + static_cast<size_t>(i) * kD;
   const int col = quarter * 128 + (tid & 15) * 8;
   const int r = tid >> 4;
-  if (tid < 16)
-    *reinterpret_cast<uint4*>(ring + static_cast<size_t>(slot) * kD + col) =
-        __ldg(reinterpret_cast<const uint4*>(fresh + col));
-  if (tid == 32 && blockIdx.y == 0) cache.ws[static_cast<size_t>(i) * kBlk + slot] = c.s[i];
-  if ((L & (kBlk - 1)) != 0) return;
-  // the block L / 128 - 1 is the ring, its newest row in slot 127
   const uint16_t sb = tid == kBlk - 1 ? c.s[i] : cache.ws[static_cast<size_t>(i) * kBlk + tid];
   uint4 x[16];
 #pragma unroll
@@ -381,22 +370,22 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const Chunk c, const Cac
   }
   const float sv = __uint_as_float(static_cast<uint32_t>(sb) << 16);
   float m = warp_max(sv);
-  if ((tid & 31) == 0) red[0][warp] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  if ((tid & 31) == 0) sm.red[0][warp] = m;
+  sync();
+  m = fmaxf(fmaxf(sm.red[0][0], sm.red[0][1]), fmaxf(sm.red[0][2], sm.red[0][3]));
   const float e = expf(sv - m);
   float z = warp_sum(e);
-  if ((tid & 31) == 0) red[1][warp] = z;
-  __syncthreads();
-  z = red[1][0] + red[1][1] + red[1][2] + red[1][3];
-  w[tid] = e / z;
-  __syncthreads();
+  if ((tid & 31) == 0) sm.red[1][warp] = z;
+  sync();
+  z = sm.red[1][0] + sm.red[1][1] + sm.red[1][2] + sm.red[1][3];
+  sm.w[tid] = e / z;
+  sync();
   float acc[8];
 #pragma unroll
   for (int a = 0; a < 8; ++a) acc[a] = 0.f;
 #pragma unroll
   for (int q = 0; q < 16; ++q) {
-    const float wi = w[q * 8 + r];
+    const float wi = sm.w[q * 8 + r];
     const uint32_t uu[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
@@ -405,15 +394,47 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const Chunk c, const Cac
     }
   }
 #pragma unroll
-  for (int a = 0; a < 8; ++a) part[r][(tid & 15) * 8 + a] = acc[a];
-  __syncthreads();
+  for (int a = 0; a < 8; ++a) sm.part[r][(tid & 15) * 8 + a] = acc[a];
+  sync();
   float tot = 0.f;
 #pragma unroll
-  for (int rr = 0; rr < 8; ++rr) tot += part[rr][tid];
-  const long long row = entry_row(cache, i, L / kBlk - 1, 213);
-  if (row < 0) return;
+  for (int rr = 0; rr < 8; ++rr) tot += sm.part[rr][tid];
+  const int j = L / kBlk - 1, page = j >> cache.page_shift;
+  int pg = -1;
+  if (page < cache.max_pages) pg = cache.table[i * cache.table_ld + page];
+  if (static_cast<unsigned>(pg) >= static_cast<unsigned>(cache.num_pages)) {
+    if (tid == 0) record_error(DEVERR_BAD_INPUT, 213);
+    return;
+  }
   __nv_bfloat16 hb = __float2bfloat16_rn(tot);
-  (which ? cache.cv : cache.ck)[row * kD + quarter * 128 + tid] = *reinterpret_cast<uint16_t*>(&hb);
+  (which ? cache.cv : cache.ck)[((static_cast<size_t>(pg) << cache.page_shift) +
+                                 (j & ((1 << cache.page_shift) - 1))) * kD + quarter * 128 + tid] =
+      *reinterpret_cast<uint16_t*>(&hb);
+}
+
+// The append of one token a sequence (ring write and, where a block completes,
+// its entry) in one launch: grid (S, 8), CTA (i, y) = (K or V, channel quarter)
+// of sequence i, 128 threads.  Latency-bound.  (hca_paged_decode_step does the
+// same inside the attention kernel for up to kInlineSeqs sequences.)
+__global__ void __launch_bounds__(kThreads) step_kernel(const Chunk c, const Cache cache) {
+  __shared__ RingScratch sm;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int i = blockIdx.x, tid = threadIdx.x;
+  const int which = blockIdx.y >> 2, quarter = blockIdx.y & 3;
+  const int L = c.ctx_len[i];
+  if (L < 1) {
+    if (tid == 0 && blockIdx.y == 0) record_error(DEVERR_BAD_INPUT, 212);
+    return;
+  }
+  const size_t row = static_cast<size_t>(i) * kBlk + ((L - 1) & (kBlk - 1));
+  if (tid < 16) {
+    const int col = quarter * 128 + tid * 8;
+    *reinterpret_cast<uint4*>((which ? cache.wv : cache.wk) + row * kD + col) =
+        __ldg(reinterpret_cast<const uint4*>((which ? c.v : c.k) + static_cast<size_t>(i) * kD + col));
+  }
+  if (tid == 32 && blockIdx.y == 0) cache.ws[row] = c.s[i];
+  if ((L & (kBlk - 1)) == 0)
+    entry_of_ring(c, cache, i, L, blockIdx.y, tid, sm, [] { __syncthreads(); });
 }
 
 }  // namespace paged

@@ -120,8 +120,10 @@ struct Params {
   int page_shift;
   // Queries that are the tokens of a chunk (chunk.q_start set; S: at most as many):
   // query i of sequence j has the window rows i + kPad j .. of the laid out raw
-  // tokens.  Else query i is sequence i, its window the ring at row 128 i.
+  // tokens.  Else query i is sequence i, its window the ring at row 128 i; with
+  // chunk.k set the call first appends token i of the chunk to `cache` (step).
   paged::Chunk chunk;
+  paged::Cache cache;
   // The kernel in front writes nothing that is read here but the window rows: only
   // the loads of those wait for it.  (An entry that it completes is not visible yet:
   // a block is seen 128 positions after its last token, and a chunk in this form has
@@ -637,10 +639,48 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto owner = [&](long long x) -> int {   // even cut: CTA of tile x
     return static_cast<int>(decode::div_nn((x + 1) * G + N - 1, N)) - 1;
   };
-  if (A0 < A1) {  // uniform across the CTA
-
   // Segments: maximal runs of this CTA's tiles inside one query.
-  const int s_first = find_seq(tiles, p.S, A0);
+  const int s_first = A0 < A1 ? find_seq(tiles, p.S, A0) : 0;
+  // A step's append, by the warps that have nothing to do until the first scores are there.
+  // The new rows go into the rings of the queries whose windows this CTA reads (one CTA a
+  // query); only the window's loads wait for that.  The entries of the blocks that the
+  // tokens complete, which no query of this call sees, are dealt out over all CTAs, a unit
+  // of K or V and channel quarter to four warps.  Against the append as a launch of its own:
+  // 148 sequences at 300 tokens 22.0 -> 20.3 us, 64 at 131072 (each completes a block) 48.6
+  // -> 47.6 us, 200 at 30000 53.7 -> 51.2 us; only many blocks at once lose, 200 at 30080
+  // (each completes one) 60.3 -> 66.7 us.
+  const bool step = p.chunk.k != nullptr && p.chunk.q_start == nullptr;
+  const bool renews = step && A0 < A1 && tiles[s_first + 1] <= A1;
+  if (step && warp > kProducers) {
+    const int t = threadIdx.x - 32 * (kProducers + 1);   // 0 .. 255
+    if (renews) {
+      for (int s = s_first; s < p.S && tiles[s + 1] <= A1; ++s) {
+        if (sL[s] < 1) continue;
+        const size_t row = static_cast<size_t>(s) * kWin + ((sL[s] - 1) & (kWin - 1));
+        if (t < 128) {
+          const size_t to = row * kDim + 8 * (t & 63), from = static_cast<size_t>(s) * kDim + 8 * (t & 63);
+          *reinterpret_cast<uint4*>((t < 64 ? p.cache.wk : p.cache.wv) + to) =
+              __ldg(reinterpret_cast<const uint4*>((t < 64 ? p.chunk.k : p.chunk.v) + from));
+        } else if (t == 128) {
+          p.cache.ws[row] = p.chunk.s[s];
+        }
+      }
+      __threadfence();           // read next by the window's copies, which go to L2
+      fence_proxy_async_all();
+      asm volatile("barrier.cta.arrive 4, %0;" ::"n"(32 * (kProducers + kSoftWarps)) : "memory");
+    }
+    const int half = t >> 7;
+    paged::RingScratch& sm = *reinterpret_cast<paged::RingScratch*>(smem + kSmemPT + 8192 * half);
+    for (long long u = 2 * cta + half; u < 8LL * p.S; u += 2 * grid) {
+      const int s = static_cast<int>(u >> 3), L = sL[s];
+      if (L >= 1 && (L & (kWin - 1)) == 0) {
+        paged::entry_of_ring(p.chunk, p.cache, s, L, static_cast<int>(u & 7), t & 127, sm,
+                             [&] { named_bar_sync(1 + half, 128); });
+        named_bar_sync(1 + half, 128);   // the scratch may be written again
+      }
+    }
+  }
+  if (A0 < A1) {  // uniform across the CTA
 
   if (warp < kProducers) {
     // ------------------------------------------------------------ producers
@@ -652,12 +692,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t boff = slab * kSlab + bx * (kSlab / boxes);
     uint32_t ua = 0, ub = 0, quse = 0;   // uses of stages 0, 1 and 2, 3 so far
     bool ok = true;
-    bool waited = !p.only_window;
+    bool waited = !p.only_window && !renews;
     // The eight slabs of a tile: entries of the page `pg` of this lane's box, or
     // (pg < 0) the window rows from y on
     auto load = [&](const CUtensorMap* map, int pg, int y) {
       if (pg < 0 && !waited) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (step) {
+          asm volatile("barrier.cta.sync 4, %0;" ::"n"(32 * (kProducers + kSoftWarps)) : "memory");
+          fence_proxy_async_all();
+        } else {
+          asm volatile("griddepcontrol.wait;" ::: "memory");
+        }
         waited = true;
       }
 #pragma unroll

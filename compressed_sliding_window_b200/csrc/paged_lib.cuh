@@ -393,17 +393,18 @@ size_t hca_paged_decode_workspace_size(int S) {
 }  // extern "C"
 
 namespace {
-// hca_paged_decode; `step`: behind the append of its tokens
+// hca_paged_decode; `step`: with the append of these tokens
 hca_status_t paged_decode(const hca_bf16* q, const hca_bf16* g, const int32_t* ctx_len, int S,
                           int H, float scale, const hca_bf16* vha_down, const hca_bf16* vha_up,
                           int vha_rank, const hca_paged_cache_t* cache, hca_bf16* out, void* ws,
-                          size_t ws_bytes, bool step, cudaStream_t stream) {
-  hca::paged::Cache c;
+                          size_t ws_bytes, const hca::paged::Chunk* step, cudaStream_t stream) {
+  namespace G = hca::paged;
+  G::Cache c;
   hca_status_t st = attend_args(q, g, out, H, scale, vha_down, vha_up, vha_rank, ws);
   if (st != HCA_OK) return st;
   if (S < 1 || ctx_len == nullptr || !aligned4(ctx_len)) return HCA_ERR_INVALID_ARG;
   if (S > 65535) return HCA_ERR_UNSUPPORTED;
-  st = paged_cache(c, cache, S, false);
+  st = paged_cache(c, cache, S, step != nullptr);
   if (st != HCA_OK) return st;
   if (ws_bytes < hca_paged_decode_workspace_size(S)) return HCA_ERR_INVALID_ARG;
   hca::pdecode::Params prm = {};
@@ -413,7 +414,14 @@ hca_status_t paged_decode(const hca_bf16* q, const hca_bf16* g, const int32_t* c
   prm.vha_down = vha_down;
   prm.vha_up = vha_up;
   prm.vha_rank = vha_rank;
-  prm.only_window = step && S <= hca::pdecode::kInlineSeqs ? 1 : 0;
+  if (step != nullptr && S <= hca::pdecode::kInlineSeqs) {
+    // one launch instead of two: both sides at the append in paged_decode_kernel
+    prm.chunk = *step;
+    prm.cache = c;
+  } else if (step != nullptr) {   // the CTAs do not have the lengths at hand
+    G::step_kernel<<<dim3(S, 8), G::kThreads, 0, stream>>>(*step, c);
+    if (cudaGetLastError() != cudaSuccess) return HCA_ERR_CUDA;
+  }
   return paged_attend(c, q, g, out, c.wk, c.wv, static_cast<uint64_t>(S) * HCA_WINDOW, prm,
                       static_cast<uint8_t*>(ws), stream);
 }
@@ -427,7 +435,7 @@ hca_status_t hca_paged_decode(const hca_bf16* q, const hca_bf16* g, const int32_
                               const hca_paged_cache_t* cache, hca_bf16* out, void* ws,
                               size_t ws_bytes, hca_stream_t stream) {
   return paged_decode(q, g, ctx_len, S, H, scale, vha_down, vha_up, vha_rank, cache, out, ws,
-                      ws_bytes, false, stream);
+                      ws_bytes, nullptr, stream);
 }
 
 hca_status_t hca_paged_decode_step(const hca_bf16* q, const hca_bf16* g, const hca_bf16* k_new,
@@ -436,19 +444,11 @@ hca_status_t hca_paged_decode_step(const hca_bf16* q, const hca_bf16* g, const h
                                    const hca_bf16* vha_down, const hca_bf16* vha_up, int vha_rank,
                                    const hca_paged_cache_t* cache, hca_bf16* out, void* ws,
                                    size_t ws_bytes, hca_stream_t stream) {
-  // validate both halves before launching either
-  hca::paged::Cache c;
-  hca_status_t st = attend_args(q, g, out, H, scale, vha_down, vha_up, vha_rank, ws);
-  if (st != HCA_OK) return st;
-  if (S < 1) return HCA_ERR_INVALID_ARG;
-  if (S > 65535) return HCA_ERR_UNSUPPORTED;
-  st = paged_cache(c, cache, S, true);
-  if (st != HCA_OK) return st;
-  if (ws_bytes < hca_paged_decode_workspace_size(S)) return HCA_ERR_INVALID_ARG;
-  st = hca_paged_append(k_new, v_new, s_new, nullptr, ctx_len, S, S, cache, stream);
-  if (st != HCA_OK) return st;
+  hca::paged::Chunk step;
+  const hca_status_t st = chunk_args(step, k_new, v_new, s_new, nullptr, ctx_len, S, S);
+  if (st != HCA_OK) return H == HCA_NUM_HEADS ? st : HCA_ERR_UNSUPPORTED;
   return paged_decode(q, g, ctx_len, S, H, scale, vha_down, vha_up, vha_rank, cache, out, ws,
-                      ws_bytes, true, stream);
+                      ws_bytes, &step, stream);
 }
 
 }  // extern "C"

@@ -436,7 +436,7 @@ hca_status_t hca_paged_decode(const hca_bf16* q, const hca_bf16* g, const int32_
 
 /*
  * hca_paged_decode_step — one serving step: hca_paged_append of one token per
- *   sequence, then hca_paged_decode, in stream order (two launches).
+ *   sequence, then hca_paged_decode; one launch for up to 512 sequences.
  */
 hca_status_t hca_paged_decode_step(const hca_bf16* q, const hca_bf16* g, const hca_bf16* k_new,
                                    const hca_bf16* v_new, const hca_bf16* s_new,
