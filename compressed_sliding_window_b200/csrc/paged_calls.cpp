@@ -8,6 +8,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/torch.h>
 
@@ -160,19 +161,17 @@ PyObject* none() {
 }
 
 using Fast = PyObject* (*)(PyObject* const*, Py_ssize_t);
-// No C++ exception leaves a call.
+// No C++ exception leaves a call: torch's own become the Python ones that the same
+// allocation would raise there (torch.OutOfMemoryError for one).
 template <Fast kCall, Py_ssize_t kArgs>
 PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != kArgs) {
     PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
     return nullptr;
   }
-  try {
-    return kCall(args, n);
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-    return nullptr;
-  }
+  HANDLE_TH_ERRORS
+  return kCall(args, n);
+  END_HANDLE_TH_ERRORS
 }
 
 // k_new, v_new, s_new, q_start | None, ctx_len, wk, wv, ws, ck, cv, table
