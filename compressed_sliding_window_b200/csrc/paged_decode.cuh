@@ -29,12 +29,15 @@
 // (The cross-lane form of decode.cuh, 124 shuffles a tile in four warps, takes
 // 4.8 us a tile of 128 keys from L2.)
 //
-// Work split.  A query that is whole inside one CTA is written straight out; one
-// that several CTAs share leaves partial results (O / l in fp32, m, l), which
-// they merge.  When giving each CTA whole queries costs at most kWholeTiles
-// tiles more than an even cut, that is done, and nothing is merged (which takes
-// about as long).  Else, with fewer queries than CTAs, each CTA has a part of one
-// query; else the key tiles of all queries laid end to end are cut evenly.
+// Work split.  A query whose keys are all one CTA's is written straight out; one
+// whose keys several CTAs share leaves partial results (O / l in fp32, m, l),
+// which they merge.  When giving each CTA whole queries costs only a few tiles
+// more than an even cut, that is done, and nothing is merged.  Else, with fewer
+// queries than CTAs, each CTA has a part of one query; else the key tiles of all
+// queries laid end to end are cut evenly.  With CTAs to spare, 2 or 4 of them take
+// the same keys and each a half or a quarter of the value columns: 64 sequences at
+// 131000 tokens 45.6 -> 39.8 us, one at 131073 20.5 -> 16.9 us, at 300 17.4 -> 12.0
+// us, eight at 40000 25.0 -> 17.1 us.
 #pragma once
 
 #include "decode.cuh"
@@ -89,8 +92,9 @@ static_assert(kAbortSlot + 4 <= 320, "barrier region overflow");
 constexpr uint32_t kTmemO = 0, kTmemS0 = 256, kTmemS1 = 320, kTmemCols = 512;
 
 // Workspace (bytes): partial O / l in fp32, [slots][64 chunks][16 heads][32
-// value columns], chunk 16 (head / 16) + column / 32; then [slots][2][64] fp32
-// (m, l) in log2 units; slots = grid + S.
+// value columns], chunk 16 (column / 128) + 4 (head / 16) + column / 32 % 4;
+// then [slots][2][64] fp32 (m, l) in log2 units (CTAs that share keys write the
+// same); slots = grid + S.
 __host__ __device__ inline size_t ws_o_bytes(int slots) {
   return static_cast<size_t>(slots) * kHeads * kDim * 4;
 }
@@ -133,7 +137,7 @@ struct Params {
 
 struct Maps {
   CUtensorMap q;    // (64, S*64, 8, 1),  box (64, 64, 8, 1): the whole q of one query
-  CUtensorMap g;    // (64, S*64, 8, 1),  box (64, 64, 4, 1): half of one query's gate
+  CUtensorMap g;    // (64, S*64, 8, 1),  box (64, 64, 2, 1): 128 columns of one query's gate
   CUtensorMap out;  // same
   CUtensorMap ck;   // (64, page, 8, pages), box (64, page, 1, 1)
   CUtensorMap cv;
@@ -350,8 +354,8 @@ __device__ __forceinline__ void own_query(const long long* tiles, int S, int lon
 
 // ---------------------------------------------------------------------------
 // Merge of a query whose tiles n CTAs share, by all of them: CTA i of the n
-// takes the chunks (16 heads x 32 value columns) [64 i / n, 64 (i + 1) / n) of
-// all n partials, once all have been written (a counter per query; a CTA waits
+// takes the i-th of n equal runs of the chunks (16 heads x 32 value columns) of
+// their column groups in all n partials, once all have been written (a counter per query; a CTA waits
 // only for those that share its first or last query, and only after its own
 // tiles).  A split's share is contiguous, so one bulk copy brings it into shared
 // memory (a CTA's own stays there from the start where its tiles are one part
@@ -365,18 +369,19 @@ __device__ __forceinline__ void own_query(const long long* tiles, int S, int lon
 constexpr int kFewSplits = 64;
 __device__ __forceinline__ int merge_room(int n) { return n <= kFewSplits ? 96 : 64; }   // chunks
 __device__ __forceinline__ uint32_t merge_data(int n) { return n <= kFewSplits ? kSmemQ : kSmemRing; }
-// first chunk and number of chunks of CTA i of n
-__device__ __forceinline__ int merge_first(int i, int n) { return 64 * i / n; }
+// first chunk of CTA i of the n that merge column groups cg .. cg + nv - 1
+__device__ __forceinline__ int merge_first(int i, int n, int cg, int nv) {
+  return 16 * cg + 16 * nv * i / n;
+}
 
-__device__ __forceinline__ void merge_query(const Params& p, int s, int c0, int n, bool kept,
-                                            uint8_t* smem, uint32_t sbase, uint32_t bar_m,
+__device__ __forceinline__ void merge_query(const Params& p, int s, size_t slot, unsigned* arrived,
+                                            int i, int n, int cg, int nv, bool kept, uint8_t* smem, uint32_t sbase, uint32_t bar_m,
                                             uint32_t& phase, volatile int* abort_flag, int warp,
                                             int lane) {
-  const int i = static_cast<int>(blockIdx.x) - c0;
-  const int k0 = merge_first(i, n), nk = merge_first(i + 1, n) - k0;
+  const int k0 = merge_first(i, n, cg, nv), nk = merge_first(i + 1, n, cg, nv) - k0;
   const int batch = nk > 0 ? min(n, merge_room(n) / nk) : n;   // splits at a time
   const uint32_t data = merge_data(n);
-  const float* po = p.ws_o + static_cast<size_t>(c0 + s) * kHeads * kDim + 512 * k0;
+  const float* po = p.ws_o + slot * kHeads * kDim + 512 * k0;
   __shared__ int late;
   auto load = [&](int f0, int f1) {   // one thread
     uint32_t bytes = 0;
@@ -395,7 +400,7 @@ __device__ __forceinline__ void merge_query(const Params& p, int s, int c0, int 
     late = 0;
     for (uint32_t k = 1;; ++k) {
       unsigned v;
-      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p.arrived + c0) : "memory");
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(arrived) : "memory");
       if (v >= static_cast<unsigned>(n)) break;
       if ((k & 63u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) {
         record_error(DEVERR_TIMEOUT, 72);
@@ -412,7 +417,7 @@ __device__ __forceinline__ void merge_query(const Params& p, int s, int c0, int 
   if (nk > 0 && !late) {
     // heads 2 lane, 2 lane + 1: M and L over the splits, every warp for itself, then the
     // weights of splits warp, warp + kWarps, ..
-    const float2* ml = reinterpret_cast<const float2*>(p.ws_ml + static_cast<size_t>(c0 + s) * 128);
+    const float2* ml = reinterpret_cast<const float2*>(p.ws_ml + slot * 128);
     float* w = reinterpret_cast<float*>(smem + (n <= kFewSplits ? kSmemPT : kSmemQ));   // [n][64]
     float2 M = make_float2(-INFINITY, -INFINITY), L = make_float2(0.f, 0.f);
 #pragma unroll 1
@@ -452,8 +457,9 @@ __device__ __forceinline__ void merge_query(const Params& p, int s, int c0, int 
     for (int r0 = 0; r0 < nk; r0 += chunks) {
       const int r = r0 + slot0, k = k0 + r;
       const bool mine = slot0 < chunks && r < nk;
-      const int h0 = 16 * (k >> 4) + (lane >> 3);               // heads h0 + 4 q
-      const size_t at = (static_cast<size_t>(s) * kHeads + h0) * kDim + 32 * (k & 15) + 4 * (lane & 7);
+      const int h0 = 16 * ((k >> 2) & 3) + (lane >> 3);         // heads h0 + 4 q
+      const size_t at = (static_cast<size_t>(s) * kHeads + h0) * kDim + 128 * (k >> 4) +
+                        32 * (k & 3) + 4 * (lane & 7);
       float acc[16];
 #pragma unroll
       for (int t = 0; t < 16; ++t) acc[t] = 0.f;
@@ -536,9 +542,9 @@ __device__ __forceinline__ void merge_query(const Params& p, int s, int c0, int 
     unsigned old;
     asm volatile("atom.add.relaxed.gpu.global.u32 %0, [%1], 1;"
                  : "=r"(old)
-                 : "l"(p.arrived + c0)
+                 : "l"(arrived)
                  : "memory");
-    if (old == 2u * n - 1) p.arrived[c0] = 0u;
+    if (old == 2u * n - 1) *arrived = 0u;
   }
 }
 
@@ -611,17 +617,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   // of all tiles laid end to end.
   const long long N = tiles[p.S];
   const int grid = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
-  const bool whole = static_cast<long long>(longest) * ((p.S + grid - 1) / grid) <=
-                     decode::div_nn(N + grid - 1, grid) + kWholeTiles;
+  const long long even = decode::div_nn(N + grid - 1, grid);
+  // Column split (lcs > 0): 2 or 4 CTAs, 1 << lcs, share the keys of a query or of a part
+  // of one and take a half or a quarter of its value columns each: the keys come from L2
+  // again, but a CTA loads less, and its epilogue and what it merges are as much shorter.
+  // Whole queries are split where that leaves no CTA with two; parts where every CTA still
+  // has one tile only.
+  int lcs = 4 * p.S <= grid ? 2 : 2 * p.S <= grid ? 1 : 0;
+  // Whole with 1 to 37 queries takes about 6 + 2.8 us a tile of the longest, with 64 of them
+  // 8 + 3.6; in parts 16.3 us with a tile a CTA and four column groups, else 13 + 5.8 us a
+  // tile of the even share.  Longest and share in tiles: 3 and 1 14.9 us whole against 16.3,
+  // 4 and 1 17.3 against 16.3; 9 and 2 33.2 against 28.7; 9 and 4 39.8 against 45.6.
+  const bool whole = lcs > 0 ? 4 * static_cast<long long>(longest) <= 7 * even + 8
+                             : static_cast<long long>(longest) * ((p.S + grid - 1) / grid) <=
+                                   even + kWholeTiles;
   const bool own = !whole && p.S < grid;
+  if (!whole) {
+    lcs = 0;
+    if (own)
+      while (lcs < 2 && (N << (lcs + 1)) <= grid && p.S < grid >> (lcs + 1)) ++lcs;
+  }
+  const int nv = kStages >> lcs;                  // 128-column groups of this CTA
+  const int cg = (cta & ((1 << lcs) - 1)) * nv;   // the first of them
+  const int vcta = cta >> lcs;                    // CTA of the split by keys
   const int G = static_cast<int>(min(static_cast<long long>(grid), max(N, 1LL)));   // even cut
   long long A0 = 0, A1 = 0;
   int mine = 0, part = 0, parts = 0;   // own: this CTA's query
-  if (whole) {
+  if (whole && lcs > 0) {
+    if (vcta < p.S) {
+      A0 = tiles[vcta];
+      A1 = tiles[vcta + 1];
+    }
+  } else if (whole) {
     A0 = tiles[decode::div_nn(static_cast<long long>(p.S) * cta, grid)];
     A1 = tiles[decode::div_nn(static_cast<long long>(p.S) * (cta + 1), grid)];
   } else if (own) {
-    own_query(tiles, p.S, longest, grid, cta, mine, part, parts);
+    own_query(tiles, p.S, longest, grid >> lcs, vcta, mine, part, parts);
     if (parts > 0) {
       const int t = static_cast<int>(tiles[mine + 1] - tiles[mine]);
       A0 = tiles[mine] + t * part / parts;
@@ -633,8 +664,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // own: this CTA's share of its own partial stays in shared memory, where nothing
   // follows its only segment, if all splits' shares fit there at once
-  const int k0 = own && parts > 1 ? merge_first(part, parts) : 0;
-  const int nk = own && parts > 1 ? merge_first(part + 1, parts) - k0 : 0;
+  const int k0 = own && parts > 1 ? merge_first(part, parts, cg, nv) : 0;
+  const int nk = own && parts > 1 ? merge_first(part + 1, parts, cg, nv) - k0 : 0;
   const bool kept = nk > 0 && parts * nk <= merge_room(parts);
   auto owner = [&](long long x) -> int {   // even cut: CTA of tile x
     return static_cast<int>(decode::div_nn((x + 1) * G + N - 1, N)) - 1;
@@ -642,10 +673,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Segments: maximal runs of this CTA's tiles inside one query.
   const int s_first = A0 < A1 ? find_seq(tiles, p.S, A0) : 0;
   // A step's append, by the warps that have nothing to do until the first scores are there.
-  // The new rows go into the rings of the queries whose windows this CTA reads (one CTA a
-  // query); only the window's loads wait for that.  The entries of the blocks that the
-  // tokens complete, which no query of this call sees, are dealt out over all CTAs, a unit
-  // of K or V and channel quarter to four warps.  Against the append as a launch of its own:
+  // The new rows go into the rings of the queries whose windows this CTA reads (CTAs that
+  // read the same one write the same); only the window's loads wait for that.  The entries
+  // of the blocks that the tokens complete, which no query of this call sees, are dealt out
+  // over all CTAs, a unit of K or V and channel quarter to four warps.  Against the append as a launch of its own:
   // 148 sequences at 300 tokens 22.0 -> 20.3 us, 64 at 131072 (each completes a block) 48.6
   // -> 47.6 us, 200 at 30000 53.7 -> 51.2 us; only many blocks at once lose, 200 at 30080
   // (each completes one) 60.3 -> 66.7 us.
@@ -690,12 +721,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int boxes = kKeyTile >> p.page_shift;
     const int bx = lane & (boxes - 1), slab = lane / boxes;
     const uint32_t boff = slab * kSlab + bx * (kSlab / boxes);
-    uint32_t ua = 0, ub = 0, quse = 0;   // uses of stages 0, 1 and 2, 3 so far
+    // Uses of the ring so far: use u takes stage u & 3, which warp u & 1 loads.  A K tile
+    // is four uses, a V tile one for each of this CTA's column groups, a gate up to two.
+    uint32_t u = 0, quse = 0;
     bool ok = true;
     bool waited = !p.only_window && !renews;
-    // The eight slabs of a tile: entries of the page `pg` of this lane's box, or
-    // (pg < 0) the window rows from y on
-    auto load = [&](const CUtensorMap* map, int pg, int y) {
+    // The eight slabs of a K tile, or those of this CTA's columns of a V tile: entries of
+    // the page `pg` of this lane's box, or (pg < 0) the window rows from y on
+    auto load = [&](const CUtensorMap* map, int pg, int y, bool values) {
       if (pg < 0 && !waited) {
         if (step) {
           asm volatile("barrier.cta.sync 4, %0;" ::"n"(32 * (kProducers + kSoftWarps)) : "memory");
@@ -705,11 +738,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         waited = true;
       }
+      const int n = values ? nv : kStages, z = values ? 2 * cg : 0;
 #pragma unroll
-      for (int i = 0; i < kStages / kProducers; ++i) {
-        const int st = kProducers * i + me;
+      for (int t = 0; t < kStages / kProducers; ++t) {
+        const int i = kProducers * t + ((u ^ me) & 1);
+        if (i >= n) break;
+        const int st = (u + i) & (kStages - 1);
         if (lane == 0) {
-          ok = ok && mbar_wait(bar(B_EMPTY + st), ((st < 2 ? ua : ub) & 1) ^ 1, abort_flag,
+          ok = ok && mbar_wait(bar(B_EMPTY + st), (((u + i) / kStages) & 1) ^ 1, abort_flag,
                                kWaitLimitNs, 40);
           if (ok) mbar_expect_tx(bar(B_FULL + st), kStage);
         }
@@ -717,12 +753,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (ok && pg >= 0 && slab < 2)
           decode::tma_load_4d_dec(sRing + st * kStage + boff, map, bar(B_FULL + st), 0, 0,
-                                  2 * st + slab, pg);
+                                  z + 2 * i + slab, pg);
         else if (ok && pg < 0 && lane == 0)
-          decode::tma_load_4d_dec(sRing + st * kStage, map, bar(B_FULL + st), 0, y, 2 * st, 0);
+          decode::tma_load_4d_dec(sRing + st * kStage, map, bar(B_FULL + st), 0, y, z + 2 * i, 0);
       }
-      ++ua;
-      ++ub;
+      u += n;
     };
     long long x = A0;
     for (int s = s_first; x < A1 && ok; ++s) {
@@ -748,37 +783,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         return j < si.nct ? box_page(p, prow, si.nc, j, bx) : -1;
       };
       int pg = page_of(j0), pg1 = j0 + 1 < j1 ? page_of(j0 + 1) : -1;
-      load(pg >= 0 ? &maps.ck : &maps.wk, pg, win);
+      load(pg >= 0 ? &maps.ck : &maps.wk, pg, win, false);
       for (int j = j0; j < j1 && ok; ++j) {
         const int pg2 = j + 2 < j1 ? page_of(j + 2) : -1;   // needed one tile later
-        if (j + 1 < j1) load(pg1 >= 0 ? &maps.ck : &maps.wk, pg1, win);
-        load(pg >= 0 ? &maps.cv : &maps.wv, pg, win);
+        if (j + 1 < j1) load(pg1 >= 0 ? &maps.ck : &maps.wk, pg1, win, false);
+        load(pg >= 0 ? &maps.cv : &maps.wv, pg, win, true);
         pg = pg1;
         pg1 = pg2;
       }
-      if (j0 == 0 && seg_end == tiles[s + 1]) {   // a whole query: its gate, into stages 0 and 1
-        if (lane == 0) {
-          ok = ok && mbar_wait(bar(B_EMPTY + me), (ua & 1) ^ 1, abort_flag, kWaitLimitNs, 43);
-          if (ok) {
-            mbar_expect_tx(bar(B_FULL + me), kStage);
-            decode::tma_load_4d_dec(sRing + me * kStage, &maps.g, bar(B_FULL + me), 0, s * kHeads,
-                                    4 * me, 0);
+      if (j0 == 0 && seg_end == tiles[s + 1]) {   // a whole query: its gate, 256 columns a stage
+        for (int i = 0; i < nv; i += 2, ++u) {
+          if ((u & 1) != static_cast<uint32_t>(me)) continue;
+          const int st = u & (kStages - 1);
+          if (lane == 0) {
+            ok = ok && mbar_wait(bar(B_EMPTY + st), ((u / kStages) & 1) ^ 1, abort_flag,
+                                 kWaitLimitNs, 43);
+            if (ok) {
+              const int boxes = min(nv, 2);
+              mbar_expect_tx(bar(B_FULL + st), 2 * kQSlab * boxes);
+              for (int b = 0; b < boxes; ++b)
+                decode::tma_load_4d_dec(sRing + st * kStage + 2 * kQSlab * b, &maps.g,
+                                        bar(B_FULL + st), 0, s * kHeads, 2 * (cg + i + b), 0);
+            }
           }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        ++ua;
       }
       x = seg_end;
     }
-    // The last copies are out: bring the gate of the rows that this CTA will merge
-    // into L2 (about the heads of its chunks: 64 part / parts ..).
-    if (own && parts > 1 && me == 0 && lane == 0) {
-      const int h0 = kHeads * part / parts, h1 = (kHeads * (part + 1) + parts - 1) / parts;
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                       p.g + (static_cast<size_t>(mine) * kHeads + h0) * kDim),
-                   "r"(static_cast<uint32_t>(min(h1, kHeads) - h0) * kDim * 2)
-                   : "memory");
-    }
+    // The last copies are out: bring the gate of the columns that this CTA will merge
+    // into L2.
+    if (own && nk > 0 && me == 0 && lane == 0)
+      for (int c = k0 >> 4; c <= (k0 + nk - 1) >> 4; ++c)
+        prefill3::tma_prefetch_4d(&maps.g, 0, mine * kHeads, 2 * c, 0);
   } else if (warp == kProducers) {
     // ------------------------------------------------------------ MMA issuer
     // The whole warp waits and walks the tiles; one elected lane issues.  Under
@@ -787,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // take from shared memory) against 115 under a branch on the lane number.
     // `ok` is uniform; after a failed wait the loops run on without waiting.
     bool ok = true;
-    uint32_t ua = 0, ub = 0, quse = 0, sidx = 0, pvidx = 0, nseg = 0;   // as the producers'
+    uint32_t u = 0, quse = 0, sidx = 0, pvidx = 0, nseg = 0;   // as the producers'
     const uint32_t idesc_s = idesc_bf16_f32(128, 64, false, false);
     const uint32_t idesc_o = idesc_bf16_f32(128, 64, true, true);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -799,40 +836,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t buf = sidx & 1;
       wait(B_SFREE + buf, ((sidx >> 1) & 1) ^ 1, 50);
       const uint32_t dS = tm + (buf ? kTmemS1 : kTmemS0);
+      const uint32_t u0 = __shfl_sync(0xffffffffu, u, 0);   // in a uniform register
 #pragma unroll 1
-      for (int st = 0; st < kStages; ++st) {
-        wait(B_FULL + st, (st < 2 ? ua : ub) & 1, 51);
+      for (int i = 0; i < kStages; ++i) {
+        const uint32_t use = u0 + i;
+        const int st = use & (kStages - 1);
+        wait(B_FULL + st, (use / kStages) & 1, 51);
         tc_fence_after();
         const uint64_t ad = sdesc_sw128(sRing + st * kStage, 16, 1024);
-        const uint64_t bd = sdesc_sw128(sQ + st * 2 * kQSlab, 16, 1024);
+        const uint64_t bd = sdesc_sw128(sQ + i * 2 * kQSlab, 16, 1024);
         if (ok && elect_one()) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)   // 16 channels each: 32 bytes on, or the next slab
             umma_bf16(dS, ad + 2 * (k & 3) + (k >> 2) * (kSlab >> 4),
-                      bd + 2 * (k & 3) + (k >> 2) * (kQSlab >> 4), idesc_s, (st | k) != 0);
+                      bd + 2 * (k & 3) + (k >> 2) * (kQSlab >> 4), idesc_s, (i | k) != 0);
           umma_commit(bar(B_EMPTY + st));
-          if (st == kStages - 1) umma_commit(bar(B_SFULL + buf));
+          if (i == kStages - 1) umma_commit(bar(B_SFULL + buf));
         }
         __syncwarp();
       }
-      ++ua;
-      ++ub;
+      u += kStages;
       ++sidx;
     };
     auto issue_pv = [&](bool first, int valid) {
       wait(B_PFULL, pvidx & 1, 52);
       if (first) wait(B_OFREE, (nseg & 1) ^ 1, 53);
       const int ksteps = (valid + 15) >> 4;
+      const uint32_t u0 = __shfl_sync(0xffffffffu, u, 0);
 #pragma unroll 1
-      for (int c = 0; c < kStages; ++c) {   // 128 value columns each
-        wait(B_FULL + c, (c < 2 ? ua : ub) & 1, 54);
+      for (int c = 0; c < nv; ++c) {   // 128 value columns each
+        const uint32_t use = u0 + c;
+        const int st = use & (kStages - 1);
+        wait(B_FULL + st, (use / kStages) & 1, 54);
         if (ok && (valid & 15) != 0) {
-          clear_rows(smem + kSmemRing + c * kStage, valid, lane);
+          clear_rows(smem + kSmemRing + st * kStage, valid, lane);
           fence_proxy_async_smem();               // read next by the tensor core
         }
         __syncwarp();
         tc_fence_after();
-        const uint64_t ad = sdesc_sw128(sRing + c * kStage, kSlab, 1024);
+        const uint64_t ad = sdesc_sw128(sRing + st * kStage, kSlab, 1024);
         const uint64_t bd = sdesc_sw128(sPT, kSlab, 1024);
         if (ok && elect_one()) {
           if (ksteps == 8) {
@@ -846,13 +888,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               umma_bf16(tm + kTmemO + 64 * c, ad + 128 * k, bd + 128 * k, idesc_o,
                         (!first || k > 0) ? 1u : 0u);
           }
-          umma_commit(bar(B_EMPTY + c));
-          if (c == kStages - 1) umma_commit(bar(B_PFREE));
+          umma_commit(bar(B_EMPTY + st));
+          if (c == nv - 1) umma_commit(bar(B_PFREE));
         }
         __syncwarp();
       }
-      ++ua;
-      ++ub;
+      u += nv;
       ++pvidx;
     };
     auto commit = [&](int b) {
@@ -879,9 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       commit(B_OFULL);
       if (j0 == 0 && seg_end == tiles[s + 1]) {   // the gate: its phases, too, pass in order
-        wait(B_FULL, ua & 1, 55);
-        wait(B_FULL + 1, ua & 1, 55);
-        ++ua;
+        for (int i = 0; i < nv; i += 2, ++u) wait(B_FULL + (u & (kStages - 1)), (u / kStages) & 1, 55);
       }
       ++nseg;
       x = seg_end;
@@ -900,7 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* smax = reinterpret_cast<float*>(smem + kSmemMax) + 128 * half;
     float* ssum = reinterpret_cast<float*>(smem + kSmemSum) + 128 * half;
     volatile int* flag = reinterpret_cast<volatile int*>(smem + kSmemFlag) + 4 * half;
-    uint32_t sidx = 0, pvidx = 0, nseg = 0, ua = 0;
+    uint32_t sidx = 0, pvidx = 0, nseg = 0, gates = 0;
     // A failed wait leaves `ok` false and the loops running (without waiting),
     // so that the four warps of a half keep meeting at their barrier.
     bool ok = true;
@@ -1005,7 +1044,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (resc) {   // rarely: this quadrant's value columns of these heads
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < nv; ++c) {
             uint32_t o[32];
             tmem_ld32(tl + kTmemO + 64 * c, o);
             tmem_wait_ld_dep32(o);
@@ -1036,7 +1075,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mrow[32 + lane] = l > 0.f ? 1.f / l : 0.f;
       __syncwarp();
       named_bar_sync(1 + half, 128);   // ssum is written again by the next segment
-      ua += 2 * (j1 - j0);             // stage 0: K and V of every tile
       // 8 or 16 heads of 128 value columns at a time, in short loops: this code
       // runs once a segment, and much of what it costs is its way into the
       // instruction cache.
@@ -1046,10 +1084,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Only now: O is complete, so every earlier use of the stages has landed,
         // and the parity names the gate's use (before, the parity of a use two
         // back would let the wait pass).
-        if (ok)
-          ok = mbar_wait_warp(bar(B_FULL), ua & 1, abort_flag, kWaitLimitNs, 63) &&
-               mbar_wait_warp(bar(B_FULL + 1), ua & 1, abort_flag, kWaitLimitNs, 63);
-        ++ua;
+        const uint32_t u = sidx * kStages + pvidx * nv + gates;
+        const int st = u & (kStages - 1);      // even where the gate takes two stages
+        for (int i = 0; i < nv && ok; i += 2)
+          ok = mbar_wait_warp(bar(B_FULL + st + (i >> 1)), (u / kStages) & 1, abort_flag,
+                              kWaitLimitNs, 63);
+        gates += (nv + 1) >> 1;
         tc_fence_after();
         // 16 heads x 32 value columns at a time through this warp's 2 KB of the P^T
         // buffer: from TMEM a thread has one column of many heads; it then takes 16
@@ -1060,9 +1100,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_row<32>(mrow + 32, inv);
         const int hr = lane >> 1, rot = (lane >> 1) & 3;     // row; order of its 4-column groups
         const int col0 = 32 * (wq & 1) + 16 * (lane & 1);    // within a 64-wide slab
-        uint8_t* grow = smem + kSmemRing + (wq >> 1) * kQSlab + (32 * half + hr) * 128;
+        uint8_t* grow = smem + kSmemRing + st * kStage + (wq >> 1) * kQSlab + (32 * half + hr) * 128;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < nv; ++c) {
           uint32_t o[32];
           tmem_ld32(tl + kTmemO + 64 * c, o);
           tmem_wait_ld_dep32(o);
@@ -1098,16 +1138,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_bar_sync(3, 32 * kSoftWarps);
         if (sw == 0 && lane == 0) {
           if (ok) {
-            prefill3::tma_store_4d(&maps.out, sRing, 0, s * kHeads, 0, 0);
-            prefill3::tma_store_4d(&maps.out, sRing + kStage, 0, s * kHeads, 4, 0);
+            for (int i = 0; i < nv; ++i)
+              prefill3::tma_store_4d(&maps.out, sRing + st * kStage + 2 * kQSlab * i, 0, s * kHeads,
+                                     2 * (cg + i), 0);
           }
           bulk_commit();
           bulk_wait_read_all();
-          mbar_arrive(bar(B_EMPTY));
-          mbar_arrive(bar(B_EMPTY + 1));
+          for (int i = 0; i < nv; i += 2) mbar_arrive(bar(B_EMPTY + st + (i >> 1)));
         }
       } else {
-        const size_t slot = static_cast<size_t>(blockIdx.x) + s;
+        const size_t slot = static_cast<size_t>(vcta) + s;
         if (wq == 0) {
           p.ws_ml[slot * 128 + 32 * half + lane] = m;
           p.ws_ml[slot * 128 + 64 + 32 * half + lane] = l;
@@ -1122,13 +1162,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         float inv[32];
         load_row<32>(mrow + 32, inv);      // before the stores, which it could not pass
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {      // value columns 128 c + key
+        for (int c = 0; c < nv; ++c) {     // value columns 128 (cg + c) + key
           uint32_t o[32];
           tmem_ld32(tl + kTmemO + 64 * c, o);
           tmem_wait_ld_dep32(o);
 #pragma unroll
           for (int hb = 0; hb < 2; ++hb) {
-            const int k = 16 * (2 * half + hb) + 4 * c + wq;
+            const int k = 16 * (cg + c) + 4 * (2 * half + hb) + wq;
             const bool here = kept && k >= k0 && k < k0 + nk;
             float* dst = here ? keep + 512 * (k - k0) : stage;
 #pragma unroll
@@ -1150,7 +1190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_bar_sync(3, 32 * kSoftWarps);
         if (sw == 0 && lane == 0)
           asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(
-                           p.arrived + (own ? cta - part : owner(tiles[s])))
+                           p.arrived + (own ? cta - (part << lcs) : owner(tiles[s])))
                        : "memory");
       }
       tc_fence_before();
@@ -1215,15 +1255,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t merges = 0;   // phase of B_MERGE
   if (own) {
     if (parts > 1)
-      merge_query(p, mine, cta - part, parts, kept, smem, sbase, bar(B_MERGE), merges, abort_flag,
-                  warp, lane);
+      merge_query(p, mine, static_cast<size_t>(vcta) - part + mine, p.arrived + cta - (part << lcs),
+                  part, parts, cg, nv, kept, smem, sbase, bar(B_MERGE), merges, abort_flag, warp,
+                  lane);
   } else if (!whole && A0 < A1) {
     // the first and the last query of this CTA may be shared with others
     const int sa = find_seq(tiles, p.S, A0), sb = find_seq(tiles, p.S, A1 - 1);
     for (int s = sa; s <= sb; s += max(sb - sa, 1)) {
       const int c0 = owner(tiles[s]), n = owner(tiles[s + 1] - 1) - c0 + 1;
       if (n > 1)
-        merge_query(p, s, c0, n, false, smem, sbase, bar(B_MERGE), merges, abort_flag, warp, lane);
+        merge_query(p, s, static_cast<size_t>(c0) + s, p.arrived + c0, cta - c0, n, 0, kStages, false,
+                    smem, sbase, bar(B_MERGE), merges, abort_flag, warp, lane);
     }
   }
   if (p.vha_rank > 0) {

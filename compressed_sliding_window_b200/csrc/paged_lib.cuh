@@ -113,8 +113,8 @@ hca_status_t paged_attend(const hca::paged::Cache& c, const hca_bf16* q, const h
   D::Maps maps;
   const uint32_t box = 1u << c.page_shift;
   bool ok = make_map4(&maps.q, q, static_cast<uint64_t>(prm.S) * HCA_NUM_HEADS, 1, 64, 8) &&
-            make_map4(&maps.g, g, static_cast<uint64_t>(prm.S) * HCA_NUM_HEADS, 1, 64, 4) &&
-            make_map4(&maps.out, out, static_cast<uint64_t>(prm.S) * HCA_NUM_HEADS, 1, 64, 4) &&
+            make_map4(&maps.g, g, static_cast<uint64_t>(prm.S) * HCA_NUM_HEADS, 1, 64, 2) &&
+            make_map4(&maps.out, out, static_cast<uint64_t>(prm.S) * HCA_NUM_HEADS, 1, 64, 2) &&
             make_map4(&maps.wk, wk, win_rows, 1, 128, 2) &&
             make_map4(&maps.wv, wv, win_rows, 1, 128, 2);
   if (ok && c.num_pages > 0) {

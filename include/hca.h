@@ -368,7 +368,7 @@ typedef struct {
  *   positions ctx_len[i] - n .. ctx_len[i] - 1.  Every block of 128 positions
  *   that they complete becomes an entry in its page, bit-identical to
  *   hca_compress of the whole sequence; the ring takes the newest tokens.
- *   q_start NULL: one token per sequence (N = S), in one launch instead of two.
+ *   q_start NULL: one token per sequence (N = S).
  * Layout:  k_new, v_new [N, 512] bf16;  s_new [N] bf16;  q_start [S + 1] and
  *          ctx_len [S] int32 on the device.  A page that is written must not
  *          be shared with another sequence (hca_pages_fork sees to that).

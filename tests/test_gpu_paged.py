@@ -219,6 +219,39 @@ def test_decode_step(P):
     c2.check_out(out2, q, g, n)
 
 
+SPLITS = [(1, 40, 300, 16), (1, 50000, 50000, 32), (1, 110000, 110000, 64), (3, 1000, 140000, 16),
+          (9, 90000, 140000, 128), (37, 1, 33000, 16), (38, 1, 40000, 64), (74, 1, 70000, 32),
+          (75, 1, 20000, 16)]
+
+
+@pytest.mark.parametrize("S,lo,hi,P", SPLITS, ids=[f"{c[0]}x{c[1]}-{c[2]}" for c in SPLITS])
+def test_decode_splits(S, lo, hi, P):
+    """Numbers of sequences and lengths at which the work is split in other ways: whole queries,
+    with 4, 2 or all column groups a CTA, and parts of queries with them."""
+    need_gpu()
+    gen = _gen(S + hi)
+    base = Seq(hi + 2, gen, "cuda")
+    L0 = [int(x) for x in np.random.default_rng(S).integers(lo, hi + 1, S)]
+    L0[-1] = hi - hi % 128 - 1                      # the step completes a block
+    c = Cache([base] * S, L0, P, room=2, seed=S)
+    n = [1] * S
+    ws = hca.paged_decode_workspace(S, "cuda")
+    k, v, s, _, ctx = c.chunk(n)
+    q, g = _qg(S, gen)
+    out = hca.paged_decode_step(q, g, k, v, s, ctx, *c.args(), workspace=ws)
+    _no_error()
+    c.check_state()
+    c.check_out(out, q, g, n)
+    assert torch.equal(hca.paged_decode(q, c.ck, c.cv, c.table, c.wk, c.wv, ctx, g, workspace=ws), out)
+    vha = tuple((torch.randn((HEADS, 5), generator=gen, device="cuda") / 8).bfloat16()
+                for _ in range(2))
+    k, v, s, _, ctx = c.chunk(n)                    # the entry just written becomes visible later
+    out = hca.paged_decode_step(q, g, k, v, s, ctx, *c.args(), workspace=ws, vha=vha)
+    _no_error()
+    c.check_state()
+    c.check_out(out, q, g, n, vha)
+
+
 def test_decode_many_sequences():
     """More sequences than each CTA plans for itself."""
     need_gpu()
