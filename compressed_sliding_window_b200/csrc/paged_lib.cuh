@@ -474,7 +474,7 @@ hca_status_t page_rows(hca::pages::Table& t, const hca_page_table_t* p) {
   return HCA_OK;
 }
 
-// Adds `n` arrays with the given lists to `m`.
+// Adds `n` arrays with the given lists to `m` (whose list length is set).
 hca_status_t move_arrays(hca::pages::Move& m, const hca_page_array_t* arrays, int n, const int* src,
                          const int* dst) {
   if (n < 0 || (n > 0 && arrays == nullptr)) return HCA_ERR_INVALID_ARG;
@@ -483,7 +483,11 @@ hca_status_t move_arrays(hca::pages::Move& m, const hca_page_array_t* arrays, in
     if (arrays[i].data == nullptr || !aligned16(arrays[i].data) || arrays[i].item_bytes < 16 ||
         arrays[i].item_bytes % 16 != 0)
       return HCA_ERR_INVALID_ARG;
-    m.a[m.arrays++] = {static_cast<uint8_t*>(arrays[i].data), arrays[i].item_bytes, src, dst};
+    const long long per = (arrays[i].item_bytes - 1) / hca::pages::kUnit + 1;
+    if (per > 0x7fffffffLL || m.units + per * m.n > 0x7fffffffLL) return HCA_ERR_UNSUPPORTED;
+    m.units += per * m.n;
+    m.a[m.arrays++] = {static_cast<uint8_t*>(arrays[i].data), arrays[i].item_bytes,
+                       static_cast<unsigned>(per), src, dst};
   }
   return HCA_OK;
 }
@@ -493,8 +497,7 @@ hca_status_t launch_move(const hca::pages::Move& m, cudaStream_t stream) {
   if (m.n < 1 || (m.arrays == 0 && m.table == nullptr)) return launch_status();
   const int sms = device_sms();
   if (sms <= 0) return HCA_ERR_CUDA;
-  long long units = 0;
-  for (int i = 0; i < m.arrays; ++i) units += (m.a[i].bytes + P::kUnit - 1) / P::kUnit * m.n;
+  long long units = m.units;
   const long long table = (static_cast<long long>(m.rows) * m.max_pages + 1023) / 1024;
   units = units > table ? units : table;
   const long long most = 8LL * sms;

@@ -369,6 +369,7 @@ constexpr int kUnit = 16384;
 struct MoveArray {
   uint8_t* base;
   long long bytes;     // of an item, a multiple of 16
+  unsigned per;        // units of an item; all units of a call are fewer than 2^31
   const int* src;      // list
   const int* dst;
 };
@@ -377,6 +378,7 @@ struct Move {
   MoveArray a[kMaxArrays];
   int arrays;
   int n;               // list length, or its upper bound
+  long long units;     // of all arrays (host)
   const int* count;    // list length on the device, or null
   // compact: table entries to renumber (null: none)
   int* table;
@@ -401,17 +403,19 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const Move m) {
       if (page >= live && page < m.num_pages) *e = m.remap[page];
     }
   }
-  long long unit0 = 0;   // first unit of the array
+  // 32-bit unit numbers: with 64-bit divisions the kernel was bound by them (48 forks: 59 % of
+  // the issue slots)
+  unsigned skip = 0;     // units of the arrays before this one, modulo the grid
   for (int q = 0; q < m.arrays; ++q) {
     const MoveArray& a = m.a[q];
-    const long long per = (a.bytes + kUnit - 1) / kUnit, units = per * n;
+    const unsigned units = a.per * static_cast<unsigned>(n);
     // this CTA's units of the array: u = blockIdx.x (mod gridDim.x), counted over all arrays
-    long long u = (blockIdx.x - unit0 % gridDim.x + gridDim.x) % gridDim.x;
-    for (; u < units; u += gridDim.x) {
-      const long long item = u / per;
+    const unsigned first = blockIdx.x >= skip ? blockIdx.x - skip : blockIdx.x + gridDim.x - skip;
+    for (unsigned u = first; u < units; u += gridDim.x) {
+      const unsigned item = u / a.per;
       const int s = a.src[item], d = a.dst[item];
       if (s < 0 || d < 0) continue;
-      const long long off = (u - item * per) * kUnit;
+      const long long off = static_cast<long long>(u - item * a.per) * kUnit;
       const int len = static_cast<int>(min(static_cast<long long>(kUnit), a.bytes - off));
       const uint4* from = reinterpret_cast<const uint4*>(a.base + s * a.bytes + off);
       uint4* to = reinterpret_cast<uint4*>(a.base + d * a.bytes + off);
@@ -427,7 +431,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const Move m) {
         if (16 * o < len) __stcs(to + o, x[k]);
       }
     }
-    unit0 += units;
+    skip = (skip + units % gridDim.x) % gridDim.x;
   }
 }
 

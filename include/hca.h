@@ -455,7 +455,8 @@ hca_status_t hca_paged_decode_step(const hca_bf16* q, const hca_bf16* g, const h
  * pairs, so results do not depend on timing.  ws: at least
  * hca_pages_workspace_size(rows, num_pages, n) bytes (n: list length, 0 where
  * there is none), 16-byte aligned, no initialisation; calls that overlap
- * need one each.
+ * need one each.  A call that may move 2^31 units of 16 KB (an item takes
+ * whole units) or more is HCA_ERR_UNSUPPORTED.
  * ------------------------------------------------------------------------- */
 typedef struct {
   int32_t* page_table;

@@ -216,6 +216,14 @@ def test_page_calls_refuse(lib):
     assert copy(n=0) == OK
 
 
+@pytest.mark.parametrize("item_bytes,n", [(1 << 62, 1), (16384 << 31, 1), (16384 << 28, 4)])
+def test_copies_past_the_units_of_a_call(lib, item_bytes, n):
+    two = (CArray * 2)(CArray(F, item_bytes), CArray(F, item_bytes))
+    st = lib.hca_pages_copy
+    st.argtypes, st.restype = [vp, i32, i32, vp, vp, i32, vp, sz, vp], i32
+    assert st(two, 2, 10, F, F, n, F, 1 << 40, None) == UNSUPPORTED
+
+
 def test_page_workspace_size(lib):
     fn = lib.hca_pages_workspace_size
     fn.restype, fn.argtypes = sz, [i32] * 3
