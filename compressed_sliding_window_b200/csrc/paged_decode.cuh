@@ -36,7 +36,7 @@
 // queries than CTAs, each CTA has a part of one query; else the key tiles of all
 // queries laid end to end are cut evenly.  With CTAs to spare, 2 or 4 of them take
 // the same keys and each a half or a quarter of the value columns: 64 sequences at
-// 131000 tokens 45.6 -> 39.8 us, one at 131073 20.5 -> 16.9 us, at 300 17.4 -> 12.0
+// 131000 tokens 45.6 -> 39.8 us, one at 131073 20.5 -> 16.9 us, at 300 17.4 -> 11.6
 // us, eight at 40000 25.0 -> 17.1 us.
 #pragma once
 
@@ -138,7 +138,6 @@ struct Params {
 struct Maps {
   CUtensorMap q;    // (64, S*64, 8, 1),  box (64, 64, 8, 1): the whole q of one query
   CUtensorMap g;    // (64, S*64, 8, 1),  box (64, 64, 2, 1): 128 columns of one query's gate
-  CUtensorMap out;  // same
   CUtensorMap ck;   // (64, page, 8, pages), box (64, page, 1, 1)
   CUtensorMap cv;
   CUtensorMap wk;   // (64, rows, 8, 1),  box (64, 128, 2, 1)
@@ -260,18 +259,6 @@ __device__ __forceinline__ void clear_rows(uint8_t* stage, int valid, int lane) 
   for (int i = valid * 8 + lane; i < end * 8; i += 32) {
     *reinterpret_cast<uint4*>(stage + i * 16) = make_uint4(0u, 0u, 0u, 0u);
     *reinterpret_cast<uint4*>(stage + kSlab + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-  }
-}
-
-template <int N>
-__device__ __forceinline__ void load_row(const float* src, float (&dst)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; i += 4) {
-    const float4 v = *reinterpret_cast<const float4*>(src + i);
-    dst[i] = v.x;
-    dst[i + 1] = v.y;
-    dst[i + 2] = v.z;
-    dst[i + 3] = v.w;
   }
 }
 
@@ -589,7 +576,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&maps.wk);
     tma_prefetch_desc(&maps.wv);
     tma_prefetch_desc(&maps.g);
-    tma_prefetch_desc(&maps.out);
   }
   if (warp == kProducers) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
@@ -722,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int bx = lane & (boxes - 1), slab = lane / boxes;
     const uint32_t boff = slab * kSlab + bx * (kSlab / boxes);
     // Uses of the ring so far: use u takes stage u & 3, which warp u & 1 loads.  A K tile
-    // is four uses, a V tile one for each of this CTA's column groups, a gate up to two.
+    // is four uses, a V tile one for each of this CTA's column groups.
     uint32_t u = 0, quse = 0;
     bool ok = true;
     bool waited = !p.only_window && !renews;
@@ -772,6 +758,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_expect_tx(bar(B_QFULL), 8 * kQSlab);
             decode::tma_load_4d_dec(sQ, &maps.q, bar(B_QFULL), 0, s * kHeads, 0, 0);
           }
+          if (j0 == 0 && seg_end == tiles[s + 1])   // a whole query: its gate, into L2
+            for (int c = cg; c < cg + nv; ++c)
+              prefill3::tma_prefetch_4d(&maps.g, 0, s * kHeads, 2 * c, 0);
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
@@ -790,24 +779,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         load(pg >= 0 ? &maps.cv : &maps.wv, pg, win, true);
         pg = pg1;
         pg1 = pg2;
-      }
-      if (j0 == 0 && seg_end == tiles[s + 1]) {   // a whole query: its gate, 256 columns a stage
-        for (int i = 0; i < nv; i += 2, ++u) {
-          if ((u & 1) != static_cast<uint32_t>(me)) continue;
-          const int st = u & (kStages - 1);
-          if (lane == 0) {
-            ok = ok && mbar_wait(bar(B_EMPTY + st), ((u / kStages) & 1) ^ 1, abort_flag,
-                                 kWaitLimitNs, 43);
-            if (ok) {
-              const int boxes = min(nv, 2);
-              mbar_expect_tx(bar(B_FULL + st), 2 * kQSlab * boxes);
-              for (int b = 0; b < boxes; ++b)
-                decode::tma_load_4d_dec(sRing + st * kStage + 2 * kQSlab * b, &maps.g,
-                                        bar(B_FULL + st), 0, s * kHeads, 2 * (cg + i + b), 0);
-            }
-          }
-          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        }
       }
       x = seg_end;
     }
@@ -919,9 +890,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                           : p.chunk.q_start != nullptr ? kWin : min(si.L, kWin));
       }
       commit(B_OFULL);
-      if (j0 == 0 && seg_end == tiles[s + 1]) {   // the gate: its phases, too, pass in order
-        for (int i = 0; i < nv; i += 2, ++u) wait(B_FULL + (u & (kStages - 1)), (u / kStages) & 1, 55);
-      }
       ++nseg;
       x = seg_end;
     }
@@ -939,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* smax = reinterpret_cast<float*>(smem + kSmemMax) + 128 * half;
     float* ssum = reinterpret_cast<float*>(smem + kSmemSum) + 128 * half;
     volatile int* flag = reinterpret_cast<volatile int*>(smem + kSmemFlag) + 4 * half;
-    uint32_t sidx = 0, pvidx = 0, nseg = 0, gates = 0;
+    uint32_t sidx = 0, pvidx = 0, nseg = 0;
     // A failed wait leaves `ok` false and the loops running (without waiting),
     // so that the four warps of a half keep meeting at their barrier.
     bool ok = true;
@@ -1075,94 +1043,79 @@ __global__ void __launch_bounds__(kThreads, 1)
       mrow[32 + lane] = l > 0.f ? 1.f / l : 0.f;
       __syncwarp();
       named_bar_sync(1 + half, 128);   // ssum is written again by the next segment
-      // 8 or 16 heads of 128 value columns at a time, in short loops: this code
-      // runs once a segment, and much of what it costs is its way into the
-      // instruction cache.
+      // The output (gate O / l of a whole query) or the partial O / l, in a short loop: this
+      // code runs once a segment, and much of what it costs is its way into the instruction
+      // cache.  A chunk of 16 heads x 32 value columns goes through this warp's 2 KB of the
+      // P^T buffer: from TMEM a thread has one column of many heads, in global memory it
+      // takes 4 columns of one head, 64 bytes in a row for 8 lanes (single columns took
+      // 4.9 us a query, and 2.8 us a partial).  The gate comes straight from L2, one step
+      // ahead; through the ring it kept the next query's tiles out of two stages (512
+      // sequences at 300 tokens 71.6 -> 66.3 us, one 11.6 -> 10.8 us).
+      // (opaque: addresses computed ahead of the tiles would spill the softmax's registers)
+      int ln = lane, sq = s;
+      asm volatile("" : "+r"(ln), "+r"(sq));
+      const size_t slot = static_cast<size_t>(vcta) + sq;
+      const int h0 = 32 * half + (ln >> 3);        // heads h0 + 16 hb + 4 q
+      const size_t at = (static_cast<size_t>(sq) * kHeads + h0) * kDim + 128 * cg + 32 * wq +
+                        4 * (ln & 7);
+      if (!direct && wq == 0) {
+        p.ws_ml[slot * 128 + 32 * half + ln] = m;
+        p.ws_ml[slot * 128 + 64 + 32 * half + ln] = l;
+      }
+      float* stage = reinterpret_cast<float*>(smem + kSmemPT) + 512 * sw;
+      float inv[8];                      // 1 / l of heads (lane >> 3) + 4 t of this half
+#pragma unroll
+      for (int t = 0; t < 8; ++t) inv[t] = mrow[32 + (ln >> 3) + 4 * t];
+      // chunk hb of the 32 heads, from dst
+      auto chunk = [&](const uint32_t(&o)[32], int hb, float* dst, float4(&v)[4]) {
+#pragma unroll
+        for (int h = 0; h < 16; ++h) dst[32 * h + ln] = __uint_as_float(o[16 * hb + h]);
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 w = reinterpret_cast<const float4*>(dst)[32 * q + ln];
+          const float f = inv[4 * hb + q];
+          v[q] = make_float4(w.x * f, w.y * f, w.z * f, w.w * f);
+        }
+        __syncwarp();
+      };
       if (direct) {
-        // out = gate O / l in place of the gate ([8 slabs][64 heads][64] swizzled)
+        uint2 gv[8];
+        auto load_gate = [&](int c, int t) {
+          gv[t] = __ldg(reinterpret_cast<const uint2*>(p.g + at + 128 * c + 4 * t * kDim));
+        };
+#pragma unroll
+        for (int t = 0; t < 8; ++t) load_gate(0, t);
         if (ok) ok = mbar_wait_warp(bar(B_OFULL), nseg & 1, abort_flag, kWaitLimitNs, 62);
-        // Only now: O is complete, so every earlier use of the stages has landed,
-        // and the parity names the gate's use (before, the parity of a use two
-        // back would let the wait pass).
-        const uint32_t u = sidx * kStages + pvidx * nv + gates;
-        const int st = u & (kStages - 1);      // even where the gate takes two stages
-        for (int i = 0; i < nv && ok; i += 2)
-          ok = mbar_wait_warp(bar(B_FULL + st + (i >> 1)), (u / kStages) & 1, abort_flag,
-                              kWaitLimitNs, 63);
-        gates += (nv + 1) >> 1;
         tc_fence_after();
-        // 16 heads x 32 value columns at a time through this warp's 2 KB of the P^T
-        // buffer: from TMEM a thread has one column of many heads; it then takes 16
-        // columns of one head, so that gate and output move 8 bytes at a time
-        // (2-byte accesses took 4.9 us a query)
-        float* stage = reinterpret_cast<float*>(smem + kSmemPT) + 512 * sw;
-        float inv[32];
-        load_row<32>(mrow + 32, inv);
-        const int hr = lane >> 1, rot = (lane >> 1) & 3;     // row; order of its 4-column groups
-        const int col0 = 32 * (wq & 1) + 16 * (lane & 1);    // within a 64-wide slab
-        uint8_t* grow = smem + kSmemRing + st * kStage + (wq >> 1) * kQSlab + (32 * half + hr) * 128;
 #pragma unroll 1
-        for (int c = 0; c < nv; ++c) {
+        for (int c = 0; c < nv; ++c) {   // value columns 128 (cg + c) + key
           uint32_t o[32];
           tmem_ld32(tl + kTmemO + 64 * c, o);
           tmem_wait_ld_dep32(o);
 #pragma unroll
           for (int hb = 0; hb < 2; ++hb) {
-#pragma unroll
-            for (int h = 0; h < 16; ++h)
-              stage[32 * h + lane] = __uint_as_float(o[16 * hb + h]) * inv[16 * hb + h];
-            __syncwarp();
             float4 v[4];
-            uint2 gv[4];
-            uint8_t* gr = grow + c * 2 * kQSlab + 16 * hb * 128;
-            auto gat = [&](int q) -> uint2* {   // 8 bytes: 4 columns from col0 + 4 (q ^ rot)
-              const int col = col0 + 4 * (q ^ rot);
-              return reinterpret_cast<uint2*>(gr + (((col >> 3) ^ (hr & 7)) << 4) + 2 * (col & 7));
-            };
+            chunk(o, hb, stage, v);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              v[q] = *reinterpret_cast<const float4*>(stage + 32 * hr + 16 * (lane & 1) +
-                                                      4 * (q ^ rot));
-              gv[q] = *gat(q);
+              const uint2 gq = gv[4 * hb + q];
+              *reinterpret_cast<uint2*>(p.out + at + 128 * c + (16 * hb + 4 * q) * kDim) =
+                  make_uint2(pack_bf16x2(v[q].x * sigmoid_fast(bf16lo_to_f32(gq.x)),
+                                         v[q].y * sigmoid_fast(bf16hi_to_f32(gq.x))),
+                             pack_bf16x2(v[q].z * sigmoid_fast(bf16lo_to_f32(gq.y)),
+                                         v[q].w * sigmoid_fast(bf16hi_to_f32(gq.y))));
+              if (c + 1 < nv) load_gate(c + 1, 4 * hb + q);
             }
-            __syncwarp();
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              *gat(q) = make_uint2(pack_bf16x2(v[q].x * sigmoid_fast(bf16lo_to_f32(gv[q].x)),
-                                               v[q].y * sigmoid_fast(bf16hi_to_f32(gv[q].x))),
-                                   pack_bf16x2(v[q].z * sigmoid_fast(bf16lo_to_f32(gv[q].y)),
-                                               v[q].w * sigmoid_fast(bf16hi_to_f32(gv[q].y))));
           }
-        }
-        fence_proxy_async_smem();
-        named_bar_sync(3, 32 * kSoftWarps);
-        if (sw == 0 && lane == 0) {
-          if (ok) {
-            for (int i = 0; i < nv; ++i)
-              prefill3::tma_store_4d(&maps.out, sRing + st * kStage + 2 * kQSlab * i, 0, s * kHeads,
-                                     2 * (cg + i), 0);
-          }
-          bulk_commit();
-          bulk_wait_read_all();
-          for (int i = 0; i < nv; i += 2) mbar_arrive(bar(B_EMPTY + st + (i >> 1)));
         }
       } else {
-        const size_t slot = static_cast<size_t>(vcta) + s;
-        if (wq == 0) {
-          p.ws_ml[slot * 128 + 32 * half + lane] = m;
-          p.ws_ml[slot * 128 + 64 + 32 * half + lane] = l;
-        }
         if (ok) ok = mbar_wait_warp(bar(B_OFULL), nseg & 1, abort_flag, kWaitLimitNs, 62);
         tc_fence_after();
         float* wo = p.ws_o + slot * kHeads * kDim;
         float* keep = reinterpret_cast<float*>(smem + merge_data(parts)) + 512 * nk * part;
-        // A chunk goes through this warp's 2 KB of the P^T buffer and leaves 16 bytes a
-        // lane: 4-byte stores to global memory took 2.8 us a partial (25 bytes a cycle).
-        float* stage = reinterpret_cast<float*>(smem + kSmemPT) + 512 * sw;
-        float inv[32];
-        load_row<32>(mrow + 32, inv);      // before the stores, which it could not pass
 #pragma unroll 1
-        for (int c = 0; c < nv; ++c) {     // value columns 128 (cg + c) + key
+        for (int c = 0; c < nv; ++c) {
           uint32_t o[32];
           tmem_ld32(tl + kTmemO + 64 * c, o);
           tmem_wait_ld_dep32(o);
@@ -1171,37 +1124,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int k = 16 * (cg + c) + 4 * (2 * half + hb) + wq;
             const bool here = kept && k >= k0 && k < k0 + nk;
             float* dst = here ? keep + 512 * (k - k0) : stage;
+            float4 v[4];
+            chunk(o, hb, dst, v);
+            float4* to = reinterpret_cast<float4*>(here ? dst : wo + 512 * k) + ln;
 #pragma unroll
-            for (int h = 0; h < 16; ++h)
-              dst[32 * h + lane] = __uint_as_float(o[16 * hb + h]) * inv[16 * hb + h];
-            if (!here) {
-              __syncwarp();
-              float4* g4 = reinterpret_cast<float4*>(wo + 512 * k) + lane;
-              float4 v[4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) v[q] = reinterpret_cast<const float4*>(stage)[32 * q + lane];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) g4[32 * q] = v[q];
-              __syncwarp();
-            }
+            for (int q = 0; q < 4; ++q) to[32 * q] = v[q];
           }
         }
-        // the partial is written: one arrival for the CTAs that share the query
-        named_bar_sync(3, 32 * kSoftWarps);
-        if (sw == 0 && lane == 0)
-          asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(
-                           p.arrived + (own ? cta - (part << lcs) : owner(tiles[s])))
-                       : "memory");
       }
+      // Everybody has left the P^T buffer, and a partial is written: one arrival for the
+      // CTAs that share the query.
+      named_bar_sync(3, 32 * kSoftWarps);
+      if (!direct && sw == 0 && lane == 0)
+        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(
+                         p.arrived + (own ? cta - (part << lcs) : owner(tiles[s])))
+                     : "memory");
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_OFREE));
       ++nseg;
       x = seg_end;
-    }
-    if (sw == 0 && lane == 0) {   // outputs stored above
-      bulk_wait_all();
-      fence_proxy_async_all();
     }
   }
 
@@ -1253,19 +1195,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   };
   uint32_t merges = 0;   // phase of B_MERGE
-  if (own) {
-    if (parts > 1)
-      merge_query(p, mine, static_cast<size_t>(vcta) - part + mine, p.arrived + cta - (part << lcs),
-                  part, parts, cg, nv, kept, smem, sbase, bar(B_MERGE), merges, abort_flag, warp,
-                  lane);
-  } else if (!whole && A0 < A1) {
-    // the first and the last query of this CTA may be shared with others
-    const int sa = find_seq(tiles, p.S, A0), sb = find_seq(tiles, p.S, A1 - 1);
+  if (own ? parts > 1 : !whole && A0 < A1) {
+    // of an even cut the first and the last query may be shared with others
+    const int sa = own ? mine : find_seq(tiles, p.S, A0);
+    const int sb = own ? mine : find_seq(tiles, p.S, A1 - 1);
+#pragma unroll 1
     for (int s = sa; s <= sb; s += max(sb - sa, 1)) {
-      const int c0 = owner(tiles[s]), n = owner(tiles[s + 1] - 1) - c0 + 1;
+      const int c0 = own ? cta - (part << lcs) : owner(tiles[s]);   // first CTA of the query
+      const int n = own ? parts : owner(tiles[s + 1] - 1) - c0 + 1;
       if (n > 1)
-        merge_query(p, s, static_cast<size_t>(c0) + s, p.arrived + c0, cta - c0, n, 0, kStages, false,
-                    smem, sbase, bar(B_MERGE), merges, abort_flag, warp, lane);
+        merge_query(p, s, static_cast<size_t>(own ? vcta - part : c0) + s, p.arrived + c0,
+                    own ? part : cta - c0, n, cg, nv, kept, smem, sbase, bar(B_MERGE), merges,
+                    abort_flag, warp, lane);
     }
   }
   if (p.vha_rank > 0) {

@@ -114,7 +114,6 @@ hca_status_t paged_attend(const hca::paged::Cache& c, const hca_bf16* q, const h
   const uint32_t box = 1u << c.page_shift;
   bool ok = make_map4(&maps.q, q, static_cast<uint64_t>(prm.S) * HCA_NUM_HEADS, 1, 64, 8) &&
             make_map4(&maps.g, g, static_cast<uint64_t>(prm.S) * HCA_NUM_HEADS, 1, 64, 2) &&
-            make_map4(&maps.out, out, static_cast<uint64_t>(prm.S) * HCA_NUM_HEADS, 1, 64, 2) &&
             make_map4(&maps.wk, wk, win_rows, 1, 128, 2) &&
             make_map4(&maps.wv, wv, win_rows, 1, 128, 2);
   if (ok && c.num_pages > 0) {
@@ -165,6 +164,18 @@ hca_status_t attend_args(const hca_bf16* q, const hca_bf16* g, const hca_bf16* o
       (vha_rank > 0 && (vha_down == nullptr || vha_up == nullptr)))
     return HCA_ERR_INVALID_ARG;
   return HCA_OK;
+}
+
+// Does `out` [rows, 64, 512] share memory with q or g?  (CTAs that split a query read both
+// while others already write.)
+bool out_overlaps(const hca_bf16* out, const hca_bf16* q, const hca_bf16* g, long long rows) {
+  const uintptr_t bytes = static_cast<uintptr_t>(rows) * HCA_NUM_HEADS * HCA_HEAD_DIM * 2;
+  const uintptr_t o = reinterpret_cast<uintptr_t>(out);
+  for (const hca_bf16* in : {q, g}) {
+    const uintptr_t i = reinterpret_cast<uintptr_t>(in);
+    if (o < i + bytes && i < o + bytes) return true;
+  }
+  return false;
 }
 
 // Which form the attention of a chunk takes.  The split form reads a sequence's entries
@@ -349,7 +360,7 @@ hca_status_t hca_paged_prefill(const hca_bf16* q, const hca_bf16* g, const hca_b
   const int most = prefill_max_clusters<true>();
   if (most <= 0) return HCA_ERR_CUDA;
   const PagedPrefillLayout L = paged_prefill_layout(S, N, most);
-  if (ws_bytes < L.total) return HCA_ERR_INVALID_ARG;
+  if (ws_bytes < L.total || out_overlaps(out, q, g, N)) return HCA_ERR_INVALID_ARG;
   uint8_t* w = static_cast<uint8_t*>(ws);
   uint16_t* raw_k = reinterpret_cast<uint16_t*>(w + L.raw_k);
   uint16_t* raw_v = reinterpret_cast<uint16_t*>(w + L.raw_v);
@@ -406,7 +417,8 @@ hca_status_t paged_decode(const hca_bf16* q, const hca_bf16* g, const int32_t* c
   if (S > 65535) return HCA_ERR_UNSUPPORTED;
   st = paged_cache(c, cache, S, step != nullptr);
   if (st != HCA_OK) return st;
-  if (ws_bytes < hca_paged_decode_workspace_size(S)) return HCA_ERR_INVALID_ARG;
+  if (ws_bytes < hca_paged_decode_workspace_size(S) || out_overlaps(out, q, g, S))
+    return HCA_ERR_INVALID_ARG;
   hca::pdecode::Params prm = {};
   prm.ctx_len = ctx_len;
   prm.S = S;

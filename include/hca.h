@@ -396,8 +396,8 @@ size_t hca_paged_prefill_workspace_size(int S, int N);
  *     keys = [entries 0 .. nc(t) - 1 ; raw keys max(0, t - 127) .. t]
  *     out  = sigmoid(g) * softmax(scale * keys . q) . values
  *   with nc(t) as above, then (vha_rank > 0) the head mix of hca_decode_vha.
- * Layout:  q, g, out [N, H, 512] bf16 (H = 64), packed as k_new; rows from
- *          q_start[S] on are not written.  vha_down, vha_up [64, vha_rank]
+ * Layout:  q, g, out [N, H, 512] bf16 (H = 64), packed as k_new; out shares no
+ *          memory with q or g; rows from q_start[S] on are not written.  vha_down, vha_up [64, vha_rank]
  *          bf16 (vha_rank = 0: none, may be NULL).  ws: at least
  *          hca_paged_prefill_workspace_size(S, N) bytes, 256-byte aligned,
  *          zero-filled before its first use (every call leaves it valid for
@@ -424,8 +424,8 @@ size_t hca_paged_decode_workspace_size(int S);
 /*
  * hca_paged_decode — hca_decode (vha_rank > 0: hca_decode_vha) over a paged
  *   cache: one query per sequence, the cache already holding its token.
- *   Reads the cache only.  q, g, out [S, 64, 512]; ws: at least
- *   hca_paged_decode_workspace_size(S) bytes, one call at a time.
+ *   Reads the cache only.  q, g, out [S, 64, 512], out apart from both; ws: at
+ *   least hca_paged_decode_workspace_size(S) bytes, one call at a time.
  * Errors:  as hca_decode_vha and hca_paged_append.
  */
 hca_status_t hca_paged_decode(const hca_bf16* q, const hca_bf16* g, const int32_t* ctx_len, int S,

@@ -279,6 +279,31 @@ def test_non_finite_tokens_stay_in_their_sequence():
                 assert ((out[i * n[0] + r].double() - ref).abs() <= bound).all()
 
 
+def test_output_over_an_input_is_refused():
+    """Before anything is launched: the cache stays as it was."""
+    need_gpu()
+    gen = _gen(51)
+    for n in ([1], [60]):
+        seq = Seq(400, gen, "cuda")
+        c = Cache([seq], [300], 16, room=n[0])
+        k, v, s, start, ctx = c.chunk(n)
+        qg = torch.randn((2 * n[0] + 1, HEADS, DIM), generator=gen, device="cuda").bfloat16()
+        q, g = qg[:n[0]], qg[n[0]:2 * n[0]]
+        before = [x.clone().nan_to_num(3.0) for x in c.args()[:5]]
+        for out in (q, g, qg[1:n[0] + 1]):
+            for given in (None, hca.paged_prefill_workspace(1, n[0], "cuda")):
+                with pytest.raises(hca.HCAError):
+                    hca.paged_prefill(q, g, k, v, s, start, ctx, *c.args(), workspace=given, out=out)
+                if n == [1]:
+                    with pytest.raises(hca.HCAError):
+                        hca.paged_decode_step(q, g, k, v, s, ctx, *c.args(), out=out)
+        assert all(torch.equal(a, b.nan_to_num(3.0)) for a, b in zip(before, c.args()))
+        out = hca.paged_prefill(q, g, k, v, s, start, ctx, *c.args(),
+                                out=torch.empty_like(qg)[:n[0]])
+        _no_error()
+        c.check_out(out, q, g, n, picks=[0, 59])
+
+
 def test_no_pages_and_one_page():
     """Sequences too short for an entry need no pool; a pool of one page holds sixteen."""
     need_gpu()
