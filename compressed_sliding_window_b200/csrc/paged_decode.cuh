@@ -1051,26 +1051,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       // 4.9 us a query, and 2.8 us a partial).  The gate comes straight from L2, one step
       // ahead; through the ring it kept the next query's tiles out of two stages (512
       // sequences at 300 tokens 71.6 -> 66.3 us, one 11.6 -> 10.8 us).
-      const size_t slot = static_cast<size_t>(vcta) + s;
-      const int h0 = 32 * half + (lane >> 3);        // heads h0 + 16 hb + 4 q
-      const size_t at = (static_cast<size_t>(s) * kHeads + h0) * kDim + 128 * cg + 32 * wq +
-                        4 * (lane & 7);
+      // (opaque: addresses computed ahead of the tiles would spill the softmax's registers)
+      int ln = lane, sq = s;
+      asm volatile("" : "+r"(ln), "+r"(sq));
+      const size_t slot = static_cast<size_t>(vcta) + sq;
+      const int h0 = 32 * half + (ln >> 3);        // heads h0 + 16 hb + 4 q
+      const size_t at = (static_cast<size_t>(sq) * kHeads + h0) * kDim + 128 * cg + 32 * wq +
+                        4 * (ln & 7);
       if (!direct && wq == 0) {
-        p.ws_ml[slot * 128 + 32 * half + lane] = m;
-        p.ws_ml[slot * 128 + 64 + 32 * half + lane] = l;
+        p.ws_ml[slot * 128 + 32 * half + ln] = m;
+        p.ws_ml[slot * 128 + 64 + 32 * half + ln] = l;
       }
       float* stage = reinterpret_cast<float*>(smem + kSmemPT) + 512 * sw;
       float inv[8];                      // 1 / l of heads (lane >> 3) + 4 t of this half
 #pragma unroll
-      for (int t = 0; t < 8; ++t) inv[t] = mrow[32 + (lane >> 3) + 4 * t];
+      for (int t = 0; t < 8; ++t) inv[t] = mrow[32 + (ln >> 3) + 4 * t];
       // chunk hb of the 32 heads, from dst
       auto chunk = [&](const uint32_t(&o)[32], int hb, float* dst, float4(&v)[4]) {
 #pragma unroll
-        for (int h = 0; h < 16; ++h) dst[32 * h + lane] = __uint_as_float(o[16 * hb + h]);
+        for (int h = 0; h < 16; ++h) dst[32 * h + ln] = __uint_as_float(o[16 * hb + h]);
         __syncwarp();
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float4 w = reinterpret_cast<const float4*>(dst)[32 * q + lane];
+          const float4 w = reinterpret_cast<const float4*>(dst)[32 * q + ln];
           const float f = inv[4 * hb + q];
           v[q] = make_float4(w.x * f, w.y * f, w.z * f, w.w * f);
         }
@@ -1123,7 +1126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float* dst = here ? keep + 512 * (k - k0) : stage;
             float4 v[4];
             chunk(o, hb, dst, v);
-            float4* to = reinterpret_cast<float4*>(here ? dst : wo + 512 * k) + lane;
+            float4* to = reinterpret_cast<float4*>(here ? dst : wo + 512 * k) + ln;
 #pragma unroll
             for (int q = 0; q < 4; ++q) to[32 * q] = v[q];
           }
