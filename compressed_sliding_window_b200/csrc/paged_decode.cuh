@@ -60,7 +60,11 @@ constexpr int kSoftWarps = 8;
 constexpr int kThreads = 32 * (kProducers + 1 + kSoftWarps);
 constexpr int kWarps = kThreads / 32;
 constexpr int kInlineSeqs = 512;    // up to this many queries each CTA plans for itself
+// Tiles that the longest CTA may have beyond an even share for whole queries to be cheaper
+// than parts of one query (80 sequences at 40000 tokens 26.7 us against 27.9) or than an even
+// cut (200 sequences at 60000 tokens 67.9 us against 81.0, at 100000 94.1 against 100.2).
 constexpr int kWholeTiles = 3;
+constexpr int kWholeTilesCut = 5;
 constexpr float kTau = 8.0f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -616,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // 4 and 1 17.3 against 16.3; 9 and 2 33.2 against 28.7; 9 and 4 39.8 against 45.6.
   const bool whole = lcs > 0 ? 4 * static_cast<long long>(longest) <= 7 * even + 8
                              : static_cast<long long>(longest) * ((p.S + grid - 1) / grid) <=
-                                   even + kWholeTiles;
+                                   even + (p.S < grid ? kWholeTiles : kWholeTilesCut);
   const bool own = !whole && p.S < grid;
   if (!whole) {
     lcs = 0;
@@ -1051,7 +1055,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // 4.9 us a query, and 2.8 us a partial).  The gate comes straight from L2, one step
       // ahead; through the ring it kept the next query's tiles out of two stages (512
       // sequences at 300 tokens 71.6 -> 66.3 us, one 11.6 -> 10.8 us).
-      // (opaque: addresses computed ahead of the tiles would spill the softmax's registers)
+      // (opaque: else the addresses are computed ahead of the tiles and more is spilled, 67.1
+      // us in place of 66.2)
       int ln = lane, sq = s;
       asm volatile("" : "+r"(ln), "+r"(sq));
       const size_t slot = static_cast<size_t>(vcta) + sq;
