@@ -19,7 +19,9 @@
 //   once the rows before the chunk have been read) and writes the item list and
 //   the copies of last pages for the attention.
 //
-// Both move bytes only: 2 KB a token in (and out again with kRaw).
+// Both move bytes only: 2 KB a token in (and out again with kRaw).  Measured: 32768
+// tokens of one sequence 13.8 us (4.9 TB/s), 32 pieces of up to 256 tokens 7.9 us, 2000
+// sequences of a token or two 73 us, of which latency is all but the first.
 #pragma once
 
 #include "compress.cuh"
