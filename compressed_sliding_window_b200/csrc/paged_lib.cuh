@@ -180,11 +180,23 @@ bool out_overlaps(const hca_bf16* out, const hca_bf16* q, const hca_bf16* g, lon
 
 // Which form the attention of a chunk takes.  The split form reads a sequence's entries
 // once per token and works on 64 rows at a time, on every SM whatever N is; the items form
-// reads them once per four tokens with 256-row tiles, but fills its 37 clusters only from
-// 148 tokens on.  One sequence at 1M tokens, GPU time: 16 tokens 61 us split, 130 us in
-// items; 64 tokens 154 and 132 us; the lines cross at 40.
-constexpr int kSplitTokens = 40;
-static_assert(kSplitTokens <= 128, "a block that the chunk completes must not become visible in it");
+// reads them once per four tokens with 256-row tiles, an item a cluster at a time (33 of
+// them).  GPU time of one sequence, split and items: 44 tokens at 20000 24.6 and 27.8 us, at
+// 1M 100 and 122; 64 tokens at 20000 24.8 and 28.2, at 131072 42.2 and 37.5, at 1M 140 and
+// 123: up to 56 split.  Of many sequences with a token or two the items fill more than one
+// round of the clusters: 32 x 2 at 40000 27.4 and 31.2, at 131072 49.0 and 45.6; 64 x 1 at
+// 20000 27.5 and 41.9, at 131072 58.5 and 72.3; but 24 x 4 at 40000 33.0 and 30.3.
+constexpr int kSplitTokens = 56;
+constexpr int kSplitTwoRounds = 74;
+constexpr int kSplitMost = 127;      // with more than two rounds
+static_assert(kSplitMost <= 128, "a block that the chunk completes must not become visible in it");
+// room for the items of N tokens: the sum of ceil(n / 4) over S sequences
+int item_room(int S, int N) { return static_cast<int>((static_cast<long long>(N) + 3LL * S) / 4); }
+bool split_form(int S, int N, int clusters) {
+  if (N <= kSplitTokens) return true;
+  const int items = item_room(S, N);
+  return (N <= kSplitTwoRounds && items > clusters) || (N <= kSplitMost && items > 2 * clusters);
+}
 constexpr int kMaxChunkSeqs = 4096;
 
 struct PagedPrefillLayout {
@@ -193,7 +205,7 @@ struct PagedPrefillLayout {
   size_t list, tail16, tail, scratch, count, raw_k, raw_v, total;
 };
 
-PagedPrefillLayout paged_prefill_layout(int S, int N, int clusters) {
+PagedPrefillLayout paged_prefill_layout(int S, int N, int clusters, bool split) {
   PagedPrefillLayout L = {};
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -201,9 +213,8 @@ PagedPrefillLayout paged_prefill_layout(int S, int N, int clusters) {
     off = align256(off + bytes);
     return at;
   };
-  L.split = N <= kSplitTokens;
-  // sum of ceil(n / 4) over S sequences with N tokens
-  L.items = static_cast<int>((static_cast<long long>(N) + 3LL * S) / 4);
+  L.split = split;
+  L.items = item_room(S, N);
   // the split form's workspace is at its start, and its head is nobody else's
   take(L.split ? hca_paged_decode_workspace_size(N) : kHeadBytes);
   if (!L.split) {
@@ -331,8 +342,8 @@ size_t hca_paged_prefill_workspace_size(int S, int N) {
   const int clusters = paged_clusters(0x7fffffff);
   if (clusters <= 0) return 0;
   // no smaller for fewer tokens: one workspace serves every call of at most S and N
-  const size_t a = paged_prefill_layout(S, N < kSplitTokens ? N : kSplitTokens, clusters).total;
-  const size_t b = N > kSplitTokens ? paged_prefill_layout(S, N, clusters).total : 0;
+  const size_t a = paged_prefill_layout(S, N < kSplitMost ? N : kSplitMost, clusters, true).total;
+  const size_t b = N > kSplitTokens ? paged_prefill_layout(S, N, clusters, false).total : 0;
   return a > b ? a : b;
 }
 
@@ -359,7 +370,7 @@ hca_status_t hca_paged_prefill(const hca_bf16* q, const hca_bf16* g, const hca_b
   const long long units = entry_units<true>(S, N);
   const int most = prefill_max_clusters<true>();
   if (most <= 0) return HCA_ERR_CUDA;
-  const PagedPrefillLayout L = paged_prefill_layout(S, N, most);
+  const PagedPrefillLayout L = paged_prefill_layout(S, N, most, split_form(S, N, most));
   if (ws_bytes < L.total || out_overlaps(out, q, g, N)) return HCA_ERR_INVALID_ARG;
   uint8_t* w = static_cast<uint8_t*>(ws);
   uint16_t* raw_k = reinterpret_cast<uint16_t*>(w + L.raw_k);

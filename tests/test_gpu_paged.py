@@ -219,6 +219,29 @@ def test_decode_step(P):
     c2.check_out(out2, q, g, n)
 
 
+FORMS = [[56], [57], [0, 40, 0, 16], [1] * 64, [2] * 37, [2] * 38, [1, 0] * 60, [1] * 127, [1] * 128,
+         [0, 3, 1] * 31]
+
+
+@pytest.mark.parametrize("n", FORMS, ids=[f"{sum(n)} of {len(n)}" for n in FORMS])
+def test_chunks_on_both_sides_of_the_forms(n):
+    """Numbers of tokens and sequences where a chunk changes from one query at a time to four
+    positions at a time, on one workspace of the largest size among them."""
+    need_gpu()
+    gen = _gen(len(n) + sum(n))
+    base = Seq(2700, gen, "cuda")
+    L0 = [int(x) for x in np.random.default_rng(len(n)).integers(0, 2600, len(n))]
+    L0[0] = 2600 - 2600 % 128 - 1
+    c = Cache([base] * len(n), L0, 16, room=max(n), seed=len(n))
+    ws = hca.paged_prefill_workspace(128, 128, "cuda")
+    k, v, s, start, ctx = c.chunk(n)
+    q, g = _qg(sum(n), gen)
+    out = hca.paged_prefill(q, g, k, v, s, start, ctx, *c.args(), workspace=ws)
+    _no_error()
+    c.check_state()
+    c.check_out(out, q, g, n)
+
+
 SPLITS = [(1, 40, 300, 16), (1, 50000, 50000, 32), (1, 110000, 110000, 64), (3, 1000, 140000, 16),
           (9, 90000, 140000, 128), (37, 1, 33000, 16), (38, 1, 40000, 64), (74, 1, 70000, 32),
           (75, 1, 20000, 16)]
