@@ -700,6 +700,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_bar_sync(1 + half, 128);   // the scratch may be written again
       }
     }
+    // A half's scratch lies in the P^T buffer, whose rows both halves write: nobody stores
+    // P before the other half's last entry is out.
+    named_bar_sync(3, 32 * kSoftWarps);
   }
   if (A0 < A1) {  // uniform across the CTA
 
