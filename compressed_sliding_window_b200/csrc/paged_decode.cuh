@@ -87,7 +87,8 @@ static_assert(kStages * kStage == kKeyTile * kDim * 2, "a tile's K or V is one r
 enum {
   B_QFULL = 0, B_QEMPTY = 1, B_FULL = 2, B_EMPTY = B_FULL + kStages, B_SFULL = B_EMPTY + kStages,
   B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2, B_PFREE = B_PFULL + 1, B_OFULL = B_PFREE + 1,
-  B_OFREE = B_OFULL + 1, B_DRAIN = B_OFREE + 1, B_MERGE = B_DRAIN + 1, B_COUNT = B_MERGE + 1
+  B_OFREE = B_OFULL + 1, B_DRAIN = B_OFREE + 1, B_MERGE = B_DRAIN + 1, B_RENEWED = B_MERGE + 1,
+  B_COUNT = B_RENEWED + 1
 };
 constexpr int kTmemSlot = 8 * B_COUNT;
 constexpr int kAbortSlot = kTmemSlot + 4;
@@ -572,6 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(B_OFREE), kSoftWarps);
     mbar_init(bar(B_DRAIN), 1);
     mbar_init(bar(B_MERGE), 1);
+    mbar_init(bar(B_RENEWED), kSoftWarps);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&maps.q);
@@ -688,7 +690,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __threadfence();           // read next by the window's copies, which go to L2
       fence_proxy_async_all();
-      asm volatile("barrier.cta.arrive 4, %0;" ::"n"(32 * (kProducers + kSoftWarps)) : "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_RENEWED));
     }
     const int half = t >> 7;
     paged::RingScratch& sm = *reinterpret_cast<paged::RingScratch*>(smem + kSmemPT + 8192 * half);
@@ -724,7 +727,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto load = [&](const CUtensorMap* map, int pg, int y, bool values) {
       if (pg < 0 && !waited) {
         if (step) {
-          asm volatile("barrier.cta.sync 4, %0;" ::"n"(32 * (kProducers + kSoftWarps)) : "memory");
+          // bounded, as all waits: a producer that gave up elsewhere is not waited for
+          ok = ok && mbar_wait_warp(bar(B_RENEWED), 0, abort_flag, kWaitLimitNs, 42);
           fence_proxy_async_all();
         } else {
           asm volatile("griddepcontrol.wait;" ::: "memory");
