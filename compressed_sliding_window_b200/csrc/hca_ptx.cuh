@@ -656,7 +656,7 @@ __device__ __forceinline__ float tanh_approx(float x) {
   return y;
 }
 
-// logistic sigmoid as 0.5 + 0.5 * tanh(x / 2): one MUFU op
+// logistic sigmoid as 0.5 + 0.5 * tanh(x / 2): one MUFU op, its error absolute (tanh's)
 __device__ __forceinline__ float sigmoid_fast(float x) {
   return fmaf(0.5f, tanh_approx(0.5f * x), 0.5f);
 }
@@ -692,6 +692,27 @@ __device__ __forceinline__ uint32_t gate_pair_bf16(float o0, float o1, float hil
       : "=f"(rl), "=f"(rh)
       : "f"(o0), "f"(o1), "f"(hil), "f"(tl), "f"(th));
   return pack_bf16x2_fwd(rl, rh);
+}
+
+// x / (1 + 2^(-g log2 e)), within 2^-19 of itself up to |g| = 12: two MUFU ops, for the paged
+// operators, whose outputs must not depend on the form a call takes.  A gate that is nearly
+// shut shows the absolute error of the two above.
+__device__ __forceinline__ float gate32(float x, float g) {
+  return __fdividef(x, 1.f + ex2_approx(-1.4426950408889634f * g));
+}
+
+// Gates below which the paged operators leave gate_pair_bf16 for gate32: tanh.approx comes in
+// steps of 2^-24 near -1, which 1 + tanh(g / 2) loses more and more to.  From here up it holds
+// 2^-11 of itself for every bf16 gate (they are all tested).  gate32 for all gates costs 2.2 us
+// an item (16 ragged chunks 252 -> 283 us), this choice by 32 gates at a time nothing.
+constexpr float kGateShut = -8.f;
+// Is one of these 32 bf16 values below `limit`?
+__device__ __forceinline__ bool any_below(const uint32_t (&g)[16], float limit) {
+  auto pair = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+  __nv_bfloat162 m = pair(g[0]);
+#pragma unroll
+  for (int i = 1; i < 16; ++i) m = __hmin2(m, pair(g[i]));
+  return fminf(__low2float(m), __high2float(m)) < limit;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {

@@ -289,11 +289,6 @@ __device__ __forceinline__ float lanes_sum32(float (&a)[32]) {
   return a[0];
 }
 
-// 1 / (1 + 2^(-x log2 e))
-__device__ __forceinline__ float sigmoid32(float x) {
-  return __fdividef(1.f, 1.f + ex2_approx(-1.4426950408889634f * x));
-}
-
 // CTAs of a query of `t` tiles when each takes at most T (or, by rounding, a tile
 // more: what counts is that all CTAs find the same)
 __device__ __forceinline__ int parts_of(int t, float inv) {
@@ -520,10 +515,10 @@ __device__ __forceinline__ void merge_query(const Params& p, int s, size_t slot,
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           *reinterpret_cast<uint2*>(p.out + at + 4 * q * kDim) =
-              make_uint2(pack_bf16x2(acc[4 * q] * sigmoid32(bf16lo_to_f32(gv[q].x)),
-                                     acc[4 * q + 1] * sigmoid32(bf16hi_to_f32(gv[q].x))),
-                         pack_bf16x2(acc[4 * q + 2] * sigmoid32(bf16lo_to_f32(gv[q].y)),
-                                     acc[4 * q + 3] * sigmoid32(bf16hi_to_f32(gv[q].y))));
+              make_uint2(pack_bf16x2(gate32(acc[4 * q], bf16lo_to_f32(gv[q].x)),
+                                     gate32(acc[4 * q + 1], bf16hi_to_f32(gv[q].x))),
+                         pack_bf16x2(gate32(acc[4 * q + 2], bf16lo_to_f32(gv[q].y)),
+                                     gate32(acc[4 * q + 3], bf16hi_to_f32(gv[q].y))));
       }
     }
   }
@@ -1113,10 +1108,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int q = 0; q < 4; ++q) {
               const uint2 gq = gv[4 * hb + q];
               *reinterpret_cast<uint2*>(p.out + at + 128 * c + (16 * hb + 4 * q) * kDim) =
-                  make_uint2(pack_bf16x2(v[q].x * sigmoid_fast(bf16lo_to_f32(gq.x)),
-                                         v[q].y * sigmoid_fast(bf16hi_to_f32(gq.x))),
-                             pack_bf16x2(v[q].z * sigmoid_fast(bf16lo_to_f32(gq.y)),
-                                         v[q].w * sigmoid_fast(bf16hi_to_f32(gq.y))));
+                  make_uint2(pack_bf16x2(gate32(v[q].x, bf16lo_to_f32(gq.x)),
+                                         gate32(v[q].y, bf16hi_to_f32(gq.x))),
+                             pack_bf16x2(gate32(v[q].z, bf16lo_to_f32(gq.y)),
+                                         gate32(v[q].w, bf16hi_to_f32(gq.y))));
               if (c + 1 < nv) load_gate(c + 1, 4 * hb + q);
             }
           }

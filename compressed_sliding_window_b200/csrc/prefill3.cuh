@@ -1169,21 +1169,33 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
               __syncwarp();
               if (lane == 0) mbar_arrive_cluster_relaxed(lbar(OFREE + ee));
             }
+            uint4* at[4];
+            uint32_t gw[16];
 #pragma unroll
-            for (int c4 = 0; c4 < 4; ++c4) {
-              const int c = 4 * (q32 & 1) + c4;   // 16-byte chunk of the 128-byte slab row
-              uint4* ptr = reinterpret_cast<uint4*>(stage + sl * 16384 + sw128_offset(row, c));
-              const uint4 gv = *ptr;
-              const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w};
-              uint32_t ow[4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int oc = 8 * c4 + 2 * q;
-                ow[q] = gate_pair_bf16(__uint_as_float(o[oc]), __uint_as_float(o[oc + 1]), hil,
-                                       gw[q]);
-              }
-              *ptr = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+            for (int c4 = 0; c4 < 4; ++c4) {   // 16-byte chunks of the 128-byte slab row
+              at[c4] = reinterpret_cast<uint4*>(stage + sl * 16384 +
+                                                sw128_offset(row, 4 * (q32 & 1) + c4));
+              *reinterpret_cast<uint4*>(gw + 4 * c4) = *at[c4];
             }
+            auto put = [&](auto&& gate) {
+#pragma unroll
+              for (int c4 = 0; c4 < 4; ++c4) {
+                uint32_t ow[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const int oc = 8 * c4 + 2 * q;
+                  ow[q] = gate(__uint_as_float(o[oc]), __uint_as_float(o[oc + 1]), gw[4 * c4 + q]);
+                }
+                *at[c4] = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+              }
+            };
+            if (kPaged && any_below(gw, kGateShut))
+              put([&](float o0, float o1, uint32_t g) {
+                return pack_bf16x2(gate32(o0 * il, bf16lo_to_f32(g)),
+                                   gate32(o1 * il, bf16hi_to_f32(g)));
+              });
+            else
+              put([&](float o0, float o1, uint32_t g) { return gate_pair_bf16(o0, o1, hil, g); });
           }
           fence_proxy_async_smem();   // this thread's writes, read next by the TMA store
           if constexpr (kVha) {       // ... or first by the VHA MMA, which also
