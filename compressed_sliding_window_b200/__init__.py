@@ -616,7 +616,8 @@ def paged_prefill(q: torch.Tensor, g: torch.Tensor, k_new: torch.Tensor, v_new: 
     """paged_append of a chunk, and the attention of its tokens over the cache.
 
     q, g [N, 64, 512], packed like k_new -> out [N, 64, 512] bf16 (memory of
-    its own; rows from q_start[S] on are not written).  The other arguments are paged_append's;
+    its own; rows before q_start[0] and from q_start[S] on are not written).
+    The other arguments are paged_append's;
     `workspace` comes from paged_prefill_workspace; `vha` as for decode."""
     if vha is None and workspace is not None:
         r = _calls().paged_prefill(q, g, k_new, v_new, s_new, q_start, ctx_len, wk, wv, ws, ck_pages,

@@ -127,10 +127,11 @@ struct Params {
   long long table_ld;
   int num_pages;
   int page_shift;
-  // Queries that are the tokens of a chunk (chunk.q_start set; S: at most as many):
-  // query i of sequence j has the window rows i + kPad j .. of the laid out raw
-  // tokens.  Else query i is sequence i, its window the ring at row 128 i; with
-  // chunk.k set the call first appends token i of the chunk to `cache` (step).
+  // Queries that are the tokens of a chunk (chunk.q_start set; S: at most as many): query i
+  // is token first + i, first = q_start[0] (what lies before is no sequence's); as one of
+  // sequence j it has the window rows first + i + kPad j .. of the laid out raw tokens.
+  // Else query i is sequence i, its window the ring at row 128 i; with chunk.k set the call
+  // first appends token i of the chunk to `cache` (step).
   paged::Chunk chunk;
   paged::Cache cache;
   // The kernel in front writes nothing that is read here but the window rows: only
@@ -176,11 +177,11 @@ __device__ __forceinline__ int seq_of(const paged::Chunk& c, int i) {
 }
 
 // Tile prefix of S queries by one CTA of NT threads, each a run of queries:
-// out[i], out[S] = total, and the longest query in *longest.  lens, rows (may be
-// null): context length and table row of each query.
+// out[i], out[S] = total, and the longest query in *longest.  first: token that is query 0 of a
+// chunk.  lens, rows (may be null): context length and table row of each query.
 template <int NT>
-__device__ __forceinline__ void plan_tiles(const Params& p, long long* out, int* lens, int* rows,
-                                           int* longest, bool report) {
+__device__ __forceinline__ void plan_tiles(const Params& p, int first, long long* out, int* lens,
+                                           int* rows, int* longest, bool report) {
   __shared__ long long wsum[NT / 32];
   __shared__ int wmax[NT / 32];
   const int S = p.S;
@@ -191,9 +192,9 @@ __device__ __forceinline__ void plan_tiles(const Params& p, long long* out, int*
   for (int i = i0; i < i1; ++i) {
     int L, row = i;
     if (p.chunk.q_start != nullptr) {
-      row = seq_of(p.chunk, i);
+      row = seq_of(p.chunk, first + i);
       const paged::Span sp = paged::span_of(p.chunk, row, false);
-      L = sp.L0 + min(max(i - sp.qs, 0), max(sp.n - 1, 0)) + 1;
+      L = sp.L0 + min(max(first + i - sp.qs, 0), max(sp.n - 1, 0)) + 1;
     } else {
       L = p.ctx_len[i];
     }
@@ -238,7 +239,7 @@ __device__ __forceinline__ void plan_tiles(const Params& p, long long* out, int*
 __global__ void __launch_bounds__(1024) plan_kernel(const Params p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ int longest;
-  plan_tiles<1024>(p, p.seq_tile, nullptr, nullptr, &longest, true);
+  plan_tiles<1024>(p, 0, p.seq_tile, nullptr, nullptr, &longest, true);
   if (threadIdx.x == 0) p.seq_tile[p.S + 1] = longest;
 }
 
@@ -547,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kSmemBar + kTmemSlot);
   long long* sT = reinterpret_cast<long long*>(smem + kSmemTiles);
   int* sL = reinterpret_cast<int*>(smem + kSmemLen);
-  __shared__ int longest;
+  __shared__ int longest, first;   // longest query in tiles; first token of a chunk
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -589,10 +590,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* sRow = reinterpret_cast<int*>(smem + kSmemRow);
   if (!p.only_window) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (inl) {
-    if (p.chunk.q_start != nullptr) p.S = min(max(p.chunk.q_start[p.chunk.S], 0), p.S);
-    plan_tiles<kThreads>(p, sT, sL, sRow, &longest, blockIdx.x == 0);
+    int skip = 0;
+    if (p.chunk.q_start != nullptr) {
+      skip = min(max(p.chunk.q_start[0], 0), p.S);
+      p.S = max(min(p.chunk.q_start[p.chunk.S], p.S) - skip, 0);
+    }
+    if (threadIdx.x == 0) first = skip;   // read behind the plan's barriers
+    plan_tiles<kThreads>(p, skip, sT, sL, sRow, &longest, blockIdx.x == 0);
   } else {
-    if (threadIdx.x == 0) longest = static_cast<int>(p.seq_tile[p.S + 1]);
+    if (threadIdx.x == 0) {
+      first = 0;
+      longest = static_cast<int>(p.seq_tile[p.S + 1]);
+    }
     __syncthreads();
   }
   tc_fence_after();
@@ -762,18 +771,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait(bar(B_QEMPTY), (quse & 1) ^ 1, abort_flag, kWaitLimitNs, 41);
           if (ok) {
             mbar_expect_tx(bar(B_QFULL), 8 * kQSlab);
-            decode::tma_load_4d_dec(sQ, &maps.q, bar(B_QFULL), 0, s * kHeads, 0, 0);
+            decode::tma_load_4d_dec(sQ, &maps.q, bar(B_QFULL), 0, (first + s) * kHeads, 0, 0);
           }
           if (j0 == 0 && seg_end == tiles[s + 1])   // a whole query: its gate, into L2
             for (int c = cg; c < cg + nv; ++c)
-              prefill3::tma_prefetch_4d(&maps.g, 0, s * kHeads, 2 * c, 0);
+              prefill3::tma_prefetch_4d(&maps.g, 0, (first + s) * kHeads, 2 * c, 0);
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
       ++quse;
       const int trow = inl ? sRow[s] : s;
       const int* prow = p.table + trow * p.table_ld;
-      const int win = p.chunk.q_start != nullptr ? s + paged::kPad * trow : s * kWin;
+      const int win = p.chunk.q_start != nullptr ? first + s + paged::kPad * trow : s * kWin;
       auto page_of = [&](int j) -> int {
         return j < si.nct ? box_page(p, prow, si.nc, j, bx) : -1;
       };
@@ -792,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // into L2.
     if (own && nk > 0 && me == 0 && lane == 0)
       for (int c = k0 >> 4; c <= (k0 + nk - 1) >> 4; ++c)
-        prefill3::tma_prefetch_4d(&maps.g, 0, mine * kHeads, 2 * c, 0);
+        prefill3::tma_prefetch_4d(&maps.g, 0, (first + mine) * kHeads, 2 * c, 0);
   } else if (warp == kProducers) {
     // ------------------------------------------------------------ MMA issuer
     // The whole warp waits and walks the tiles; one elected lane issues.  Under
@@ -1062,6 +1071,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int ln = lane, sq = s;
       asm volatile("" : "+r"(ln), "+r"(sq));
       const size_t slot = static_cast<size_t>(vcta) + sq;
+      sq += first;
       const int h0 = 32 * half + (ln >> 3);        // heads h0 + 16 hb + 4 q
       const size_t at = (static_cast<size_t>(sq) * kHeads + h0) * kDim + 128 * cg + 32 * wq +
                         4 * (ln & 7);
@@ -1211,7 +1221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int c0 = own ? cta - (part << lcs) : owner(tiles[s]);   // first CTA of the query
       const int n = own ? parts : owner(tiles[s + 1] - 1) - c0 + 1;
       if (n > 1)
-        merge_query(p, s, static_cast<size_t>(own ? vcta - part : c0) + s, p.arrived + c0,
+        merge_query(p, first + s, static_cast<size_t>(own ? vcta - part : c0) + s, p.arrived + c0,
                     own ? part : cta - c0, n, cg, nv, kept, smem, sbase, bar(B_MERGE), merges,
                     abort_flag, warp, lane);
     }
@@ -1224,6 +1234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint16_t* mix = reinterpret_cast<uint16_t*>(fu + kHeads * kHeads);   // 1 KB per warp
     decode::vha_load_factors<kThreads>(p, fd, fu);
     __syncthreads();
+    p.out += static_cast<size_t>(first) * kHeads * kDim;
     decode::vha_mix_columns<kThreads>(p, fd, fu, mix + warp * kHeads * 8, warp, lane);
   }
 }

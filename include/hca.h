@@ -397,8 +397,9 @@ size_t hca_paged_prefill_workspace_size(int S, int N);
  *     out  = sigmoid(g) * softmax(scale * keys . q) . values
  *   with nc(t) as above, then (vha_rank > 0) the head mix of hca_decode_vha.
  * Layout:  q, g, out [N, H, 512] bf16 (H = 64), packed as k_new; out shares no
- *          memory with q or g; rows from q_start[S] on are not written.  vha_down, vha_up [64, vha_rank]
- *          bf16 (vha_rank = 0: none, may be NULL).  ws: at least
+ *          memory with q or g; rows before q_start[0] and from q_start[S] on
+ *          are not written.  vha_down, vha_up [64, vha_rank] bf16
+ *          (vha_rank = 0: none, may be NULL).  ws: at least
  *          hca_paged_prefill_workspace_size(S, N) bytes, 256-byte aligned,
  *          zero-filled before its first use (every call leaves it valid for
  *          the next, whatever its S and N); calls that overlap need one each.
