@@ -85,6 +85,7 @@ def lib() -> ctypes.CDLL:
         L.hca_pages_workspace_size.argtypes = [i, i, i]
         L.hca_pages_workspace_size.restype = sz
         L.hca_pages_resize.argtypes = [pt, vp, vp, sz, vp]
+        L.hca_pages_resize_copy.argtypes = [pt, vp, pa, i, vp, sz, vp]
         L.hca_pages_fork.argtypes = [pt, vp, vp, vp, i, pa, i, pa, i, vp, vp, sz, vp]
         L.hca_pages_compact.argtypes = [pt, pa, i, vp, vp, sz, vp]
         L.hca_pages_copy.argtypes = [pa, i, i, vp, vp, i, vp, sz, vp]
@@ -98,8 +99,8 @@ def lib() -> ctypes.CDLL:
                      "hca_quantize_e4m3", "hca_decode_e4m3", "hca_prefill_fwd_vha",
                      "hca_decode_vha", "hca_prefill_bwd", "hca_paged_append",
                      "hca_paged_prefill", "hca_paged_decode", "hca_paged_decode_step",
-                     "hca_pages_resize", "hca_pages_fork", "hca_pages_compact",
-                     "hca_pages_copy"):
+                     "hca_pages_resize", "hca_pages_resize_copy", "hca_pages_fork",
+                     "hca_pages_compact", "hca_pages_copy"):
             getattr(L, name).restype = i
         _LIB = L
     return _LIB
@@ -732,21 +733,33 @@ def _pages_workspace(workspace, rows, num_pages, n, device):
 
 def resize_pages(page_table: torch.Tensor, n_pages: torch.Tensor, ref: torch.Tensor,
                  entries: torch.Tensor, page_size: int,
-                 workspace: Optional[torch.Tensor] = None) -> None:
+                 workspace: Optional[torch.Tensor] = None, pools=()) -> None:
     """Give every row of the page table the pages of entries[r] entries, in place.
 
     page_table [R, max_pages], n_pages [R], ref [num_pages], entries [R], all
     int32 on the device.  0 frees a row, a negative number leaves it.  Rows
     shrink first; rows that grow take the lowest free pages, row by row, while
-    there are any (n_pages[r] tells what row r has)."""
-    r = _calls().resize_pages(page_table, n_pages, ref, entries, page_size, workspace)
-    if r is not False:
-        return None if r is None else _raise("hca_pages_resize", r)
+    there are any (n_pages[r] tells what row r has).
+
+    A row that is cut inside a page it shares with a branch may only be
+    appended to with a page of its own: pass the `pools` ([num_pages, ...]
+    tensors), and its partly used page is replaced by a copy in each of them.
+    (Without them the row keeps the shared page, which then must not be
+    written.)  Where no page is free for that, device_error() reports it and
+    the row keeps the shared page."""
+    if not len(pools):
+        r = _calls().resize_pages(page_table, n_pages, ref, entries, page_size, workspace)
+        if r is not False:
+            return None if r is None else _raise("hca_pages_resize", r)
     device = _device_of(page_table, "page_table")
     table, rows, num = _page_table(page_table, n_pages, ref, page_size, device)
     pe = _need(entries, "entries", (rows,), torch.int32, device)
     workspace = _pages_workspace(workspace, rows, num, 0, device)
-    _call(device, "hca_pages_resize", table, pe, *_workspace(workspace, device))
+    if len(pools):
+        _call(device, "hca_pages_resize_copy", table, pe, _page_arrays(pools, num, "pools", device),
+              len(pools), *_workspace(workspace, device))
+    else:
+        _call(device, "hca_pages_resize", table, pe, *_workspace(workspace, device))
 
 
 def fork_pages(page_table: torch.Tensor, n_pages: torch.Tensor, ref: torch.Tensor,

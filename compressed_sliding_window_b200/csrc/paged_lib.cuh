@@ -530,16 +530,45 @@ hca_status_t launch_move(const hca::pages::Move& m, cudaStream_t stream) {
   return launch_status();
 }
 
+hca_status_t pages_resize(const hca_page_table_t* table, const int32_t* entries,
+                          const hca_page_array_t* pools, int n_pools, bool copy, void* ws,
+                          size_t ws_bytes, cudaStream_t stream) {
+  namespace P = hca::pages;
+  P::Table t;
+  hca_status_t st = page_rows(t, table);
+  if (st != HCA_OK) return st;
+  if (entries == nullptr || ws == nullptr || !aligned4(entries) || !aligned16(ws) ||
+      ws_bytes < hca_pages_workspace_size(t.rows, t.num_pages, 0) || (copy && n_pools < 1))
+    return HCA_ERR_INVALID_ARG;
+  int* free_list = static_cast<int*>(ws);
+  int* prefix = free_list + t.num_pages;
+  P::Move m = {};
+  int *src = nullptr, *dst = nullptr, *count = nullptr;
+  if (copy) {
+    src = prefix + t.rows + 1;
+    dst = src + t.rows;
+    count = dst + t.rows;
+    m.n = t.rows;
+    m.count = count;
+    st = move_arrays(m, pools, n_pools, src, dst);
+    if (st != HCA_OK) return st;
+  }
+  P::resize_kernel<<<1, P::kPlanThreads, 0, stream>>>(t, entries, free_list, prefix, src, dst,
+                                                      count);
+  st = launch_status();
+  return st == HCA_OK && copy ? launch_move(m, stream) : st;
+}
+
 }  // namespace
 
 extern "C" {
 
 size_t hca_pages_workspace_size(int rows, int num_pages, int n) {
   if (rows < 1 || num_pages < 1 || n < 0) return 0;
-  // the largest of: resize (free list, prefix), fork (four lists), compact (two half lists,
-  // remap, count), copy (marks, two lists)
+  // the largest of: resize (free list, prefix, two lists, count), fork (four lists), compact
+  // (two half lists, remap, count), copy (marks, two lists)
   const size_t pages = num_pages, list = n;
-  const size_t resize = pages + rows + 1, fork = 4 * list, compact = 2 * (pages / 2 + 1) + pages + 1,
+  const size_t resize = pages + 3 * static_cast<size_t>(rows) + 2, fork = 4 * list, compact = 2 * (pages / 2 + 1) + pages + 1,
                copy = pages + 2 * list;
   size_t most = resize;
   for (const size_t x : {fork, compact, copy}) most = x > most ? x : most;
@@ -548,17 +577,13 @@ size_t hca_pages_workspace_size(int rows, int num_pages, int n) {
 
 hca_status_t hca_pages_resize(const hca_page_table_t* table, const int32_t* entries, void* ws,
                               size_t ws_bytes, hca_stream_t stream) {
-  namespace P = hca::pages;
-  P::Table t;
-  const hca_status_t st = page_rows(t, table);
-  if (st != HCA_OK) return st;
-  if (entries == nullptr || ws == nullptr || !aligned4(entries) || !aligned16(ws) ||
-      ws_bytes < hca_pages_workspace_size(t.rows, t.num_pages, 0))
-    return HCA_ERR_INVALID_ARG;
-  int* free_list = static_cast<int*>(ws);
-  P::resize_kernel<<<1, P::kPlanThreads, 0, stream>>>(t, entries, free_list,
-                                                      free_list + t.num_pages);
-  return launch_status();
+  return pages_resize(table, entries, nullptr, 0, false, ws, ws_bytes, stream);
+}
+
+hca_status_t hca_pages_resize_copy(const hca_page_table_t* table, const int32_t* entries,
+                                   const hca_page_array_t* pools, int n_pools, void* ws,
+                                   size_t ws_bytes, hca_stream_t stream) {
+  return pages_resize(table, entries, pools, n_pools, true, ws, ws_bytes, stream);
 }
 
 hca_status_t hca_pages_fork(const hca_page_table_t* table, const int32_t* parents,

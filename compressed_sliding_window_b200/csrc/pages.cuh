@@ -107,7 +107,13 @@ __device__ __forceinline__ void drop_ref(const Table& t, int page) {
 // many as it has).  First every row that shrinks gives its last pages back,
 // then rows that grow take the lowest free pages, row by row, while there are
 // any; n_pages tells what each row got.
-// Workspace: free list [num_pages], growth prefix [rows + 1].
+// With `src` (lists of pages to copy, for move_kernel) a row whose last page is
+// now partly used, and named by other rows too, gets a fresh page in its place
+// before any row grows, so that what is appended to it stays its own; of rows
+// that share that page with nobody else the last one keeps it.  Without a free
+// page it keeps the shared one, which is reported.
+// Workspace: free list [num_pages], growth prefix [rows + 1]; then src, dst
+// [rows] and their length.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ int clamped_pages(const Table& t, int r) {
   const int n = t.n_pages[r];
@@ -117,7 +123,8 @@ __device__ __forceinline__ int clamped_pages(const Table& t, int r) {
 
 __global__ void __launch_bounds__(kPlanThreads)
     resize_kernel(const Table t, const int* __restrict__ entries, int* __restrict__ free_list,
-                  int* __restrict__ prefix) {
+                  int* __restrict__ prefix, int* __restrict__ src, int* __restrict__ dst,
+                  int* __restrict__ count) {
   __shared__ int red[kPlanWarps];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   // growth of every row, and its prefix
@@ -155,11 +162,62 @@ __global__ void __launch_bounds__(kPlanThreads)
     if (lane == 0) t.n_pages[r] = have + d;
   }
   __syncthreads();
-  if (grown == 0) return;
-  const int got = scan_pages(
-      t.ref, 0, t.num_pages, grown, red, [](int c) { return c <= 0; },
+  // rows that need their partly used page for themselves
+  int own = 0;
+  auto partial = [&](int r) -> int {   // that page, or -1
+    const int e = entries[r], c = e >> t.page_shift;
+    if (e <= 0 || (e & ((1 << t.page_shift) - 1)) == 0 || c >= min(t.n_pages[r], t.max_pages))
+      return -1;
+    const int page = t.table[r * t.ld + c];
+    return static_cast<unsigned>(page) < static_cast<unsigned>(t.num_pages) &&
+                   __ldcg(t.ref + page) > 1
+               ? page
+               : -1;
+  };
+  if (src != nullptr) {
+    for (int r = threadIdx.x; r < t.rows; r += kPlanThreads) dst[r] = partial(r);
+    __syncthreads();
+    for (int base = 0; base < t.rows; base += kPlanThreads) {
+      const int r = base + threadIdx.x;
+      const int page = r < t.rows ? dst[r] : -1;
+      int left = 0;                    // references of it when it is this row's turn
+      if (page >= 0) {
+        left = __ldcg(t.ref + page);
+        for (int q = 0; q < r; ++q) left -= dst[q] == page ? 1 : 0;
+      }
+      int total;
+      const int k = own + block_scan(left > 1 ? 1 : 0, red, &total);
+      if (left > 1) src[k] = r;        // the row, for now
+      own += total;
+    }
+  }
+  if (grown + own == 0) {
+    if (src != nullptr && threadIdx.x == 0) *count = 0;
+    return;
+  }
+  const int found = scan_pages(
+      t.ref, 0, t.num_pages, grown + own, red, [](int c) { return c <= 0; },
       [&](int k, int page) { free_list[k] = page; });
   __syncthreads();
+  if (src != nullptr) {
+    for (int k = threadIdx.x; k < own; k += kPlanThreads) {
+      const int r = src[k];
+      int* at = t.table + r * t.ld + (entries[r] >> t.page_shift);
+      if (k < found) {
+        src[k] = *at;
+        dst[k] = free_list[k];
+        drop_ref(t, *at);
+        t.ref[free_list[k]] = 1;
+        *at = free_list[k];
+      } else {
+        src[k] = dst[k] = -1;
+        record_error(DEVERR_BAD_INPUT, 228);
+      }
+    }
+    if (threadIdx.x == 0) *count = own;
+  }
+  const int got = max(found - own, 0);
+  free_list += own;
   for (int r = w; r < t.rows; r += kPlanWarps) {
     const int first = prefix[r];
     if (first < 0) continue;

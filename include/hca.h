@@ -371,7 +371,8 @@ typedef struct {
  *   q_start NULL: one token per sequence (N = S).
  * Layout:  k_new, v_new [N, 512] bf16;  s_new [N] bf16;  q_start [S + 1] and
  *          ctx_len [S] int32 on the device.  A page that is written must not
- *          be shared with another sequence (hca_pages_fork sees to that).
+ *          be shared with another sequence (hca_pages_fork and, for a sequence
+ *          that is cut, hca_pages_resize_copy see to that).
  * Errors:  HCA_ERR_INVALID_ARG for S < 1, N < 0, a NULL or misaligned pointer,
  *          q_start NULL with N != S; HCA_ERR_UNSUPPORTED for another page size
  *          or a table of more than 2^31 / 128 entries a row.  On the device:
@@ -490,6 +491,22 @@ size_t hca_pages_workspace_size(int rows, int num_pages, int n);
  */
 hca_status_t hca_pages_resize(const hca_page_table_t* table, const int32_t* entries, void* ws,
                               size_t ws_bytes, hca_stream_t stream);
+
+/*
+ * hca_pages_resize_copy — hca_pages_resize that leaves every row free to be
+ *   appended to.  A row cut to a number of entries that ends inside a page
+ *   which other rows name too (a branch cut below the place where it left its
+ *   parent, or a parent below a branch) would go on writing into their page.
+ *   Here it gets a fresh page, with the contents copied in each of the `pools`
+ *   (as for hca_pages_fork), before any row grows; of rows that share such a
+ *   page with nobody else, the last keeps it.
+ * Errors:  those of hca_pages_resize, HCA_ERR_INVALID_ARG for n_pools < 1; on
+ *          the device a row for which no page is free keeps the shared page,
+ *          which is reported.
+ */
+hca_status_t hca_pages_resize_copy(const hca_page_table_t* table, const int32_t* entries,
+                                   const hca_page_array_t* pools, int n_pools, void* ws,
+                                   size_t ws_bytes, hca_stream_t stream);
 
 /*
  * hca_pages_fork — branch sequences: the empty row children[i] becomes a copy
