@@ -442,11 +442,19 @@ _CALLS = None
 
 
 def _calls():
-    """The compiled module (linked against libhca.so, which must be built)."""
+    """The compiled module (linked against libhca.so, which must be built, and torch)."""
     global _CALLS
     if _CALLS is None:
         lib()
-        from . import _paged_calls
+        rebuild = ("build it for torch " + torch.__version__ + " with "
+                   "`python -m compressed_sliding_window_b200.build`")
+        try:
+            from . import _paged_calls
+        except ImportError as e:
+            raise RuntimeError(f"_paged_calls cannot be loaded ({e}): {rebuild}") from e
+        built = getattr(_paged_calls, "torch_version", "another version")
+        if built != str(torch.__version__):
+            raise RuntimeError(f"_paged_calls was built for torch {built}: {rebuild}")
         _CALLS = _paged_calls
     return _CALLS
 

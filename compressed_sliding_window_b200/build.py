@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(PKG_DIR, "libhca.so")
 MAIN_SRC = os.path.join(CSRC, "hca_lib.cu")
 CALLS_PATH = os.path.join(PKG_DIR, "_paged_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 CALLS_SRC = os.path.join(CSRC, "paged_calls.cpp")
+CALLS_STAMP = CALLS_PATH + ".stamp"     # what CALLS_PATH was built against
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -46,11 +47,27 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(s) <= lib_m for s in _sources())
 
 
+def _built_against() -> str:
+    import torch
+    return (f"torch {torch.__version__}, C++11 ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, "
+            f"Python {sys.version.split()[0]}\n")
+
+
+def calls_up_to_date() -> bool:
+    """Newer than its sources, and built against the torch and Python that run: the module uses
+    torch's C++ interface, which another version need not share."""
+    if not os.path.exists(CALLS_PATH) or not os.path.exists(CALLS_STAMP):
+        return False
+    with open(CALLS_STAMP) as f:
+        if f.read() != _built_against():
+            return False
+    return all(os.path.getmtime(f) <= os.path.getmtime(CALLS_PATH)
+               for f in (CALLS_SRC, os.path.join(ROOT, "include", "hca.h")))
+
+
 def build_calls(force: bool = False, verbose: bool = False) -> str:
     """The module behind the binding's paged calls (needs libhca.so)."""
-    srcs = [CALLS_SRC, os.path.join(ROOT, "include", "hca.h")]
-    if not force and os.path.exists(CALLS_PATH) and all(
-            os.path.getmtime(f) <= os.path.getmtime(CALLS_PATH) for f in srcs):
+    if not force and calls_up_to_date():
         return CALLS_PATH
     import torch
     base = os.path.join(os.path.dirname(torch.__file__))
@@ -58,6 +75,7 @@ def build_calls(force: bool = False, verbose: bool = False) -> str:
     tmp = CALLS_PATH + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DHCA_TORCH_VERSION="{torch.__version__}"',
            "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(base, "include"),
            "-I" + os.path.join(base, "include", "torch", "csrc", "api", "include"),
            "-I" + os.path.join(cuda, "include"), CALLS_SRC, "-o", tmp, "-L" + PKG_DIR,
@@ -69,6 +87,8 @@ def build_calls(force: bool = False, verbose: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, CALLS_PATH)
+    with open(CALLS_STAMP, "w") as f:
+        f.write(_built_against())
     return CALLS_PATH
 
 

@@ -367,4 +367,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged_calls", nullptr, -1, method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__paged_calls(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__paged_calls(void) {
+  PyObject* m = PyModule_Create(&module);
+  // the torch that it was built against; the binding compares
+  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", HCA_TORCH_VERSION) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
