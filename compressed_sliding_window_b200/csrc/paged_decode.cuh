@@ -589,8 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool inl = p.S <= kInlineSeqs;
   int* sRow = reinterpret_cast<int*>(smem + kSmemRow);
   if (!p.only_window) asm volatile("griddepcontrol.wait;" ::: "memory");
+  int skip = 0;   // first token of a chunk
   if (inl) {
-    int skip = 0;
     if (p.chunk.q_start != nullptr) {
       skip = min(max(p.chunk.q_start[0], 0), p.S);
       p.S = max(min(p.chunk.q_start[p.chunk.S], p.S) - skip, 0);
@@ -672,10 +672,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The new rows go into the rings of the queries whose windows this CTA reads (CTAs that
   // read the same one write the same); only the window's loads wait for that.  The entries
   // of the blocks that the tokens complete, which no query of this call sees, are dealt out
-  // over all CTAs, a unit of K or V and channel quarter to four warps.  Against the append as a launch of its own:
-  // 148 sequences at 300 tokens 22.0 -> 20.3 us, 64 at 131072 (each completes a block) 48.6
-  // -> 47.6 us, 200 at 30000 53.7 -> 51.2 us; only many blocks at once lose, 200 at 30080
-  // (each completes one) 60.3 -> 66.7 us.
+  // over all CTAs, a unit of K or V and channel quarter to four warps.  Against the append as
+  // a launch of its own: 148 sequences at 300 tokens 22.0 -> 20.3 us, 64 at 131072 (each
+  // completes a block) 48.6 -> 47.6 us, 200 at 30000 53.7 -> 51.2 us; only many blocks at once
+  // lose, 200 at 30080 (each completes one) 60.3 -> 66.7 us.  The host picks the form and does
+  // not know the lengths; even sequences in lockstep complete their blocks in one step of 128.
   const bool step = p.chunk.k != nullptr && p.chunk.q_start == nullptr;
   const bool renews = step && A0 < A1 && tiles[s_first + 1] <= A1;
   if (step && warp > kProducers) {
@@ -771,18 +772,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait(bar(B_QEMPTY), (quse & 1) ^ 1, abort_flag, kWaitLimitNs, 41);
           if (ok) {
             mbar_expect_tx(bar(B_QFULL), 8 * kQSlab);
-            decode::tma_load_4d_dec(sQ, &maps.q, bar(B_QFULL), 0, (first + s) * kHeads, 0, 0);
+            decode::tma_load_4d_dec(sQ, &maps.q, bar(B_QFULL), 0, (skip + s) * kHeads, 0, 0);
           }
           if (j0 == 0 && seg_end == tiles[s + 1])   // a whole query: its gate, into L2
             for (int c = cg; c < cg + nv; ++c)
-              prefill3::tma_prefetch_4d(&maps.g, 0, (first + s) * kHeads, 2 * c, 0);
+              prefill3::tma_prefetch_4d(&maps.g, 0, (skip + s) * kHeads, 2 * c, 0);
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
       ++quse;
       const int trow = inl ? sRow[s] : s;
       const int* prow = p.table + trow * p.table_ld;
-      const int win = p.chunk.q_start != nullptr ? first + s + paged::kPad * trow : s * kWin;
+      const int win = p.chunk.q_start != nullptr ? skip + s + paged::kPad * trow : s * kWin;
       auto page_of = [&](int j) -> int {
         return j < si.nct ? box_page(p, prow, si.nc, j, bx) : -1;
       };
@@ -801,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // into L2.
     if (own && nk > 0 && me == 0 && lane == 0)
       for (int c = k0 >> 4; c <= (k0 + nk - 1) >> 4; ++c)
-        prefill3::tma_prefetch_4d(&maps.g, 0, (first + mine) * kHeads, 2 * c, 0);
+        prefill3::tma_prefetch_4d(&maps.g, 0, (skip + mine) * kHeads, 2 * c, 0);
   } else if (warp == kProducers) {
     // ------------------------------------------------------------ MMA issuer
     // The whole warp waits and walks the tiles; one elected lane issues.  Under
@@ -1011,6 +1012,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int h = 0; h < 32; ++h) lsum[h] *= mrow[32 + h];
           }
         }
+        // P is rounded to bf16 (half a step, 2^-8 of each probability): the MMA takes it with
+        // V, in V's type.  The row sums add the 32-bit values.  Outputs are 2.3e-3 from the
+        // 64-bit result in place of 1.7e-3, which the rounding of the output alone gives.
         uint32_t pk[16];
 #pragma unroll
         for (int h = 0; h < 32; h += 2) {

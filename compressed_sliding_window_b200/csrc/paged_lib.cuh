@@ -185,9 +185,12 @@ bool out_overlaps(const hca_bf16* out, const hca_bf16* q, const hca_bf16* g, lon
 // 1M 100 and 122; 64 tokens at 20000 24.8 and 28.2, at 131072 42.2 and 37.5, at 1M 140 and
 // 123: up to 56 split.  Of many sequences with a token or two the items fill more than one
 // round of the clusters: 32 x 2 at 40000 27.4 and 31.2, at 131072 49.0 and 45.6; 64 x 1 at
-// 20000 27.5 and 41.9, at 131072 58.5 and 72.3; but 24 x 4 at 40000 33.0 and 30.3.
+// 20000 27.5 and 41.9, at 131072 58.5 and 72.3; but 24 x 4 at 40000 33.0 and 30.3.  With two
+// rounds the limit is half of the 148 SMs: up to there the split form has two CTAs for each
+// query, which share its value columns.  (Where long contexts would rather have the items, as
+// 32 x 2 at 131072 by 7 %, the host cannot tell: the lengths are on the device.)
 constexpr int kSplitTokens = 56;
-constexpr int kSplitTwoRounds = 74;
+constexpr int kSplitTwoRounds = 148 / 2;
 constexpr int kSplitMost = 127;      // with more than two rounds
 static_assert(kSplitMost <= 128, "a block that the chunk completes must not become visible in it");
 // room for the items of N tokens: the sum of ceil(n / 4) over S sequences

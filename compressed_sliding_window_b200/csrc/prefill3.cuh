@@ -628,7 +628,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             ok = mbar_wait_cluster_warp(bar(PFREE + slot), ((sj >> 1) & 1) ^ 1, abort_flag,
                                         kWaitLimitNs, 331);
           uint8_t* const gdst = pscr + slot * kSlot;
-          // pass B: probabilities into the scratch slot
+          // pass B: probabilities into the scratch slot, rounded to bf16 (half a step, 2^-8 of
+          // each: the MMA takes them with V, in V's type); the row sums add the 32-bit values
           float rs = 0.f;
 #pragma unroll 1
           for (int cc = 0; ok && cc < nh; cc += 32) {
