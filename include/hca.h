@@ -428,7 +428,8 @@ size_t hca_paged_decode_workspace_size(int S);
  *   cache: one query per sequence, the cache already holding its token.
  *   Reads the cache only.  q, g, out [S, 64, 512], out apart from both; ws: at
  *   least hca_paged_decode_workspace_size(S) bytes, one call at a time.
- * Errors:  as hca_decode_vha and hca_paged_append.
+ * Errors:  as hca_decode_vha and hca_paged_append; HCA_ERR_UNSUPPORTED for
+ *          S > 65535.
  */
 hca_status_t hca_paged_decode(const hca_bf16* q, const hca_bf16* g, const int32_t* ctx_len, int S,
                               int H, float scale, const hca_bf16* vha_down,
